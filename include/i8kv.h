@@ -412,6 +412,101 @@ i8kv_status i8kv_bf16_paged_decode_attn(void* out, int out_dtype, const uint16_t
                                         int max_blocks, int num_blocks, float softmax_scale, int partition,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Block-scaled INT8 KV cache.  The pages of the INT8 cache, but one fp32     */
+/* scale per (16-token block, KV head) for K and one for V:                   */
+/*     K cache  int8 [NB, Hkv, D/16, 16, 16]     V cache  int8 [NB, Hkv, D, 16] */
+/*     K / V scale  fp32 [NB, Hkv]               value = code x scale           */
+/* The scales take 1/16 of the bytes of per-token ones, and a block's scale is */
+/* one number for a whole 16-token contraction step.                          */
+/* These entry points accept D in {64, 128, 256}, any Hkv up to 256 and any    */
+/* G = Hq / Hkv.  Two sequences must not share a block that a call writes.     */
+/*                                                                             */
+/* i8kv_block_kv_write, i8kv_block_kv_read: a ragged batch.  Sequence b covers */
+/* rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of the call (cu_tokens int32      */
+/* [B + 1], not decreasing, cu_tokens[B] <= T); they are the last positions of */
+/* its seq_lens[b] tokens (seq_lens counts them).  cu_tokens == NULL: one row  */
+/* per sequence (T = B), and seq_lens[b] <= 0 marks an unused one.  Rows from   */
+/* cu_tokens[B] on belong to no sequence: they are not read and not written.    */
+/* Rows that do not fit their sequence (offsets out of [0, T], more rows than   */
+/* seq_lens[b], a length above max_blocks * 16) are skipped and recorded in     */
+/* the device error word (2), like table entries outside the pool.             */
+/*                                                                             */
+/* Writing.  Per touched block and KV head, each step one fp32 operation:       */
+/*   s = max(s_old, max|x| / 127) over the call's tokens of the block; s_old is */
+/*       the stored scale when the block holds tokens before the call's first   */
+/*       (they stand at lower offsets), else 0: offset 0 begins a block anew;   */
+/*   new tokens:    code = round_half_even(x / s)  (s = 0: code 0);             */
+/*   lower offsets: code = round_half_even(code x (s_old / s)) when s > s_old.  */
+/* Codes behind the call's last token of a block stay as they are.  Inputs must */
+/* be finite.  k, v: bf16 rows [Hkv, D], k_stride / v_stride elements apart     */
+/* (multiples of 8; 16-byte aligned), e.g. slices of a fused projection.        */
+/*                                                                             */
+/* Reading back: k_out, v_out [T, Hkv, D] (out_dtype) = code x scale, one fp32  */
+/* product, rounded to nearest-even bf16 with I8KV_OUT_BF16.                    */
+/* One launch each.                                                             */
+/* ------------------------------------------------------------------------ */
+i8kv_status i8kv_block_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int T,
+                                const int32_t* cu_tokens, const int32_t* seq_lens, const int32_t* block_tables, int B,
+                                int Hkv, int D, int block_size, int max_blocks, int num_blocks, int8_t* k_cache,
+                                int8_t* v_cache, float* k_scale, float* v_scale, void* stream);
+
+i8kv_status i8kv_block_kv_read(void* k_out, void* v_out, int out_dtype, int T, const int32_t* cu_tokens,
+                               const int32_t* seq_lens, const int32_t* block_tables, int B, int Hkv, int D,
+                               int block_size, int max_blocks, int num_blocks, const int8_t* k_cache,
+                               const int8_t* v_cache, const float* k_scale, const float* v_scale, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Decode attention over the block-scaled cache.  For sequence b (its newest  */
+/* token is position L - 1, L = seq_lens[b]) and query head h, over the keys   */
+/* max(0, key_begin[b], L - window) <= t < L:                                  */
+/*   s_t = softmax_scale q . K_t;   softcap > 0: s_t = softcap tanh(s_t/softcap) */
+/*   s_t = s_t - alibi_slopes[h] (L - 1 - t)                                   */
+/*   out[b, h] = sum_t softmax(s)_t V_t                                        */
+/* q: bf16 rows [B] of [Hq, D], q_stride elements apart (a multiple of 8).      */
+/* key_begin int32 [B], alibi_slopes fp32 [Hq]: nullable.  window = 0: none.   */
+/* softcap = 0: none, else in [1e-3, 1e4] (its scores carry an absolute error  */
+/* of about softcap x 2^-21).  softmax_scale <= 0 selects 1/sqrt(D).           */
+/* A sequence without a visible key gives a zero row.                          */
+/* Nothing of a hidden block is read, and hidden tokens of a visible block     */
+/* count as absent.  fp32 outputs keep about 20 bits of the weights, bf16       */
+/* outputs 12.  V scales below 2^-100 count as 2^-100.                          */
+/* workspace: at least i8kv_block_decode_workspace_bytes(...) bytes, 16-byte   */
+/* aligned, no initialization; the rules of the other decode calls apply        */
+/* (reuse on one stream; overlapping calls and graphs need their own).          */
+/* Two launches.                                                               */
+/* ------------------------------------------------------------------------ */
+size_t i8kv_block_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks);
+
+i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
+                                   const int8_t* v_cache, const float* k_scale, const float* v_scale,
+                                   const int32_t* block_tables, const int32_t* seq_lens, const int32_t* key_begin,
+                                   const float* alibi_slopes, int B, int Hq, int Hkv, int D, int block_size,
+                                   int max_blocks, int num_blocks, float softmax_scale, float softcap, int window,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Chunk attention over the block-scaled cache: the same scores for a chunk of */
+/* one sequence.  Row j (position history_len + j) sees the keys               */
+/*   max(0, key_begin[j], history_len + j - window + 1) <= t < key_end[j]       */
+/* with key_begin nullable (0), key_end nullable (history_len + j + 1, causal)  */
+/* and cut at history_len + chunk_len.  key_begin masks packed documents,       */
+/* key_end beyond the row a prefix that every row sees.  The distance is        */
+/* |history_len + j - t|.  Every key, the chunk's own among them, is read from  */
+/* the cache (i8kv_block_kv_write first) through block_table (int32, covering   */
+/* history_len + chunk_len positions).  Rows without a visible key are zero.    */
+/* q: bf16 rows [chunk_len] of [Hq, D], q_stride elements apart (a multiple of   */
+/* 8).  out [chunk_len, Hq, D].  The rest as for i8kv_block_decode_attn.         */
+/* ------------------------------------------------------------------------ */
+size_t i8kv_block_prefix_workspace_bytes(int history_len, int chunk_len, int Hq, int Hkv, int D);
+
+i8kv_status i8kv_block_prefix_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
+                                   const int8_t* v_cache, const float* k_scale, const float* v_scale,
+                                   const int32_t* block_table, int history_len, int chunk_len, const int32_t* key_begin,
+                                   const int32_t* key_end, const float* alibi_slopes, int Hq, int Hkv, int D,
+                                   int block_size, int num_blocks, float softmax_scale, float softcap, int window,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,6 +33,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
 
 _SIGS = {
     "i8kv_last_error": [ctypes.c_char_p, _Z],
@@ -59,6 +60,14 @@ _SIGS = {
     "i8kv_debug_qk_i32": [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P],
     "i8kv_bf16_kv_write": [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P],
     "i8kv_bf16_kv_prefix_attn": [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _Z, _P],
+    "i8kv_block_kv_write": [_P, _P, _L, _L, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P],
+    "i8kv_block_kv_read": [_P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P],
+    "i8kv_block_decode_workspace_bytes": [_I, _I, _I, _I, _I],
+    "i8kv_block_decode_attn": [_P, _I, _P, _L, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F, _I,
+                               _P, _Z, _P],
+    "i8kv_block_prefix_workspace_bytes": [_I, _I, _I, _I, _I],
+    "i8kv_block_prefix_attn": [_P, _I, _P, _L, _P, _P, _P, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I,
+                               _P, _Z, _P],
     "i8kv_bf16_paged_decode_attn": [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _Z, _P],
 }
 
@@ -81,6 +90,8 @@ def lib():
             fn.restype = _I
         L.i8kv_decode_workspace_bytes.restype = _Z
         L.i8kv_prefix_workspace_bytes.restype = _Z
+        L.i8kv_block_decode_workspace_bytes.restype = _Z
+        L.i8kv_block_prefix_workspace_bytes.restype = _Z
         _lib = L
     return _lib
 
@@ -416,3 +427,196 @@ def prefill_chunk(out, q, k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale
         _ptr(q_scale, torch.float32, "q_scale"), _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
         ctypes.byref(route), _stream(stream)))
     return int(route.value)
+
+
+# ----------------------------------------------------------------------------- block-scaled cache
+def alloc_block_cache(num_blocks: int, Hkv: int, D: int, device="cuda"):
+    """Zeroed block-scaled INT8 cache tensors: the INT8 cache's pages, one scale per (block, KV head)."""
+    return dict(
+        k_cache=torch.zeros((num_blocks, Hkv, D // 16, BLOCK_SIZE, 16), dtype=torch.int8, device=device),
+        v_cache=torch.zeros((num_blocks, Hkv, D, BLOCK_SIZE), dtype=torch.int8, device=device),
+        k_scale=torch.zeros((num_blocks, Hkv), dtype=torch.float32, device=device),
+        v_scale=torch.zeros((num_blocks, Hkv), dtype=torch.float32, device=device),
+    )
+
+
+def _require(cond: bool, msg: str):
+    if not cond:
+        raise I8KVError(ERR_INVALID_ARG, msg)
+
+
+def _at(t, dtype, shape, dev, name) -> int | None:
+    """Device address of a contiguous tensor of exactly this dtype, shape and device (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise I8KVError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
+                                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
+    return t.data_ptr()
+
+
+def _rows(t, shape, dev, name):
+    """(address, row stride in elements) of bf16 rows [N, H, D]: each row contiguous, the rows any stride apart."""
+    if t.dtype is not torch.bfloat16 or t.device != dev or t.shape != shape:
+        raise I8KVError(ERR_INVALID_ARG, f"{name} must be a torch.bfloat16 tensor of shape {tuple(shape)} on {dev}, "
+                                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    n, h, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
+    st = t.stride()
+    _require((st[2] == 1 or d == 1) and (st[1] == d or h == 1), f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (st[0] if n > 1 else h * d)
+
+
+def _block_geom(k_cache, v_cache, k_scale, v_scale):
+    """(addresses, NB, Hkv, D, device) of a block-scaled cache."""
+    NB, Hkv, D = _cache_geom(k_cache, 16)
+    dev = k_cache.device
+    _require(dev.type == "cuda", "k_cache must be a CUDA tensor")
+    return (_at(k_cache, torch.int8, k_cache.shape, dev, "k_cache"),
+            _at(v_cache, torch.int8, (NB, Hkv, D, BLOCK_SIZE), dev, "v_cache"),
+            _at(k_scale, torch.float32, (NB, Hkv), dev, "k_scale"),
+            _at(v_scale, torch.float32, (NB, Hkv), dev, "v_scale")), NB, Hkv, D, dev
+
+
+def _call(fn, dev, stream, *args):
+    """Run a C entry point on `stream` (the device's current one when None) with the tensors' device current."""
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        _require(stream.device == dev, f"stream is on {stream.device}, the tensors on {dev}")
+        handle = stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, handle))
+
+
+def _ragged(seq_lens, block_tables, cu_tokens, T, dev):
+    _require(block_tables.dim() == 2, "block_tables must be [B, max_blocks]")
+    B, mb = block_tables.shape
+    _require(cu_tokens is not None or T == B, f"{T} rows for {B} sequences need cu_tokens")
+    return (_at(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), _at(seq_lens, torch.int32, (B,), dev, "seq_lens"),
+            _at(block_tables, torch.int32, (B, mb), dev, "block_tables"), B, mb)
+
+
+def block_kv_write(k, v, seq_lens, block_tables, k_cache, v_cache, k_scale, v_scale, cu_tokens=None, stream=None):
+    """Quantize k, v (bf16 [T, Hkv, D]; rows may be strided) into the block-scaled cache.
+
+    Sequence b brings rows cu_tokens[b] .. cu_tokens[b + 1] - 1, its last positions; seq_lens [B]
+    counts them.  Without cu_tokens every sequence brings one row.  A block whose scale grows has
+    its older codes rescaled (see include/i8kv.h for the rounding)."""
+    cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
+    T = k.shape[0]
+    kp, ks = _rows(k, (T, Hkv, D), dev, "k")
+    vp, vs = _rows(v, (T, Hkv, D), dev, "v")
+    cu, sl, bt, B, mb = _ragged(seq_lens, block_tables, cu_tokens, T, dev)
+    _call(lib().i8kv_block_kv_write, dev, stream, kp, vp, ks, vs, T, cu, sl, bt, B, Hkv, D, BLOCK_SIZE, mb, NB, *cache)
+
+
+def block_kv_read(k_out, v_out, seq_lens, block_tables, k_cache, v_cache, k_scale, v_scale, cu_tokens=None, stream=None):
+    """k_out, v_out [T, Hkv, D] (float32 or bfloat16) <- code x scale of the last cu_tokens[b + 1] - cu_tokens[b]
+    positions of every sequence (one without cu_tokens); rows of no sequence are left as they were."""
+    cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
+    T = k_out.shape[0]
+    code = _out_code(k_out)
+    kp = _at(k_out, k_out.dtype, (T, Hkv, D), dev, "k_out")
+    vp = _at(v_out, k_out.dtype, (T, Hkv, D), dev, "v_out")
+    cu, sl, bt, B, mb = _ragged(seq_lens, block_tables, cu_tokens, T, dev)
+    _call(lib().i8kv_block_kv_read, dev, stream, kp, vp, code, T, cu, sl, bt, B, Hkv, D, BLOCK_SIZE, mb, NB, *cache)
+
+
+def _out_code(t) -> int:
+    _require(t.dtype in (torch.float32, torch.bfloat16), f"out must be float32 or bfloat16, got {t.dtype}")
+    return OUT_F32 if t.dtype is torch.float32 else OUT_BF16
+
+
+def _workspace(workspace, need: int, dev, stream):
+    """(address, bytes) of the given workspace, or of one allocated for this call on its stream."""
+    if workspace is None:
+        if stream is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _require(workspace.device == dev and workspace.is_contiguous(), f"workspace must be contiguous on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _device_bytes(fn, dev, *args) -> int:
+    """A workspace size (it depends on the device's number of SMs)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return int(fn(*args))
+    with torch.cuda.device(dev):
+        return int(fn(*args))
+
+
+def block_decode_workspace(B: int, Hq: int, Hkv: int, D: int, max_blocks: int, device="cuda") -> torch.Tensor:
+    """A block_decode_attn workspace (reusable by later calls on the same stream)."""
+    dev = torch.device(device)
+    n = _device_bytes(lib().i8kv_block_decode_workspace_bytes, dev, B, Hq, Hkv, D, max_blocks)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def block_decode_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, workspace=None,
+                      softmax_scale: float = 0.0, softcap: float = 0.0, window: int = 0, key_begin=None,
+                      alibi_slopes=None, stream=None):
+    """out [B, Hq, D] (float32 or bfloat16) <- decode attention of q (bf16 [B, Hq, D]; rows may be strided)
+    over the block-scaled cache.
+
+    softcap: scores pass through softcap * tanh(. / softcap).  alibi_slopes (float32 [Hq]): a bias of
+    -slope * (seq_len - 1 - t).  window: only the last `window` keys.  key_begin (int32 [B]): only keys from there
+    on.  workspace: a block_decode_workspace(...) tensor; when None one is allocated for this call."""
+    cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
+    _require(q.dim() == 3, "q must be [B, Hq, D]")
+    B, Hq = q.shape[0], q.shape[1]
+    qp, qs = _rows(q, (B, Hq, D), dev, "q")
+    op = _at(out, out.dtype, (B, Hq, D), dev, "out")
+    code = _out_code(out)
+    _, sl, bt, Bt, mb = _ragged(seq_lens, block_tables, None, B, dev)
+    kb = _at(key_begin, torch.int32, (B,), dev, "key_begin")
+    al = _at(alibi_slopes, torch.float32, (Hq,), dev, "alibi_slopes")
+    need = 0
+    if workspace is None:
+        need = _device_bytes(lib().i8kv_block_decode_workspace_bytes, dev, B, Hq, Hkv, D, mb)
+    ws, n = _workspace(workspace, need, dev, stream)
+    _call(lib().i8kv_block_decode_attn, dev, stream, op, code, qp, qs, *cache, bt, sl, kb, al, B, Hq, Hkv, D, BLOCK_SIZE,
+          mb, NB, softmax_scale, softcap, window, ws.data_ptr(), n)
+
+
+def block_prefix_workspace(history_len: int, chunk_len: int, Hq: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
+    """A block_prefix_attn workspace (reusable by later calls on the same stream)."""
+    dev = torch.device(device)
+    n = _device_bytes(lib().i8kv_block_prefix_workspace_bytes, dev, history_len, chunk_len, Hq, Hkv, D)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+
+
+def block_prefix_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_table, history_len: int, workspace=None,
+                      softmax_scale: float = 0.0, softcap: float = 0.0, window: int = 0, key_begin=None, key_end=None,
+                      alibi_slopes=None, stream=None):
+    """out [C, Hq, D] (float32 or bfloat16) <- attention of a chunk's rows q (bf16 [C, Hq, D], positions
+    history_len ..; rows may be strided) over one sequence of the block-scaled cache, the chunk's own keys included.
+
+    Row j sees keys max(key_begin[j], position - window + 1) .. key_end[j] - 1 (int32 [C] each, optional; causal
+    without key_end).  softcap, alibi_slopes and workspace as in block_decode_attn."""
+    cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
+    _require(q.dim() == 3, "q must be [C, Hq, D]")
+    C, Hq = q.shape[0], q.shape[1]
+    qp, qs = _rows(q, (C, Hq, D), dev, "q")
+    op = _at(out, out.dtype, (C, Hq, D), dev, "out")
+    code = _out_code(out)
+    history_len = int(history_len)
+    _require(block_table.dim() == 1 and block_table.shape[0] * BLOCK_SIZE >= history_len + C,
+             f"block_table must be 1-D and cover {history_len + C} positions")
+    bt = _at(block_table, torch.int32, block_table.shape, dev, "block_table")
+    kb = _at(key_begin, torch.int32, (C,), dev, "key_begin")
+    ke = _at(key_end, torch.int32, (C,), dev, "key_end")
+    al = _at(alibi_slopes, torch.float32, (Hq,), dev, "alibi_slopes")
+    need = 0
+    if workspace is None:
+        need = _device_bytes(lib().i8kv_block_prefix_workspace_bytes, dev, history_len, C, Hq, Hkv, D)
+    ws, n = _workspace(workspace, need, dev, stream)
+    _call(lib().i8kv_block_prefix_attn, dev, stream, op, code, qp, qs, *cache, bt, history_len, C, kb, ke, al, Hq, Hkv, D,
+          BLOCK_SIZE, NB, softmax_scale, softcap, window, ws.data_ptr(), n)

@@ -71,7 +71,8 @@ i8kv_status i8kv_device_error(int* code) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return from_cuda(e, "i8kv_device_error: synchronize");
   int v = 0;
-  cudaError_t (*readers[])(int*) = {i8kv::read_error_producer, i8kv::read_error_decode, i8kv::read_error_prefix};
+  cudaError_t (*readers[])(int*) = {i8kv::read_error_producer, i8kv::read_error_decode, i8kv::read_error_prefix,
+                                    i8kv::read_error_block_cache, i8kv::read_error_block_decode};
   for (auto rd : readers) {
     int x = 0;
     e = rd(&x);
@@ -526,6 +527,200 @@ i8kv_status i8kv_bf16_paged_decode_attn(void* out, int out_dtype, const uint16_t
                                 workspace_bytes, out, out_dtype);
   if (s != I8KV_OK || B == 0) return s;
   return from_cuda(i8kv::launch_bf16_decode(p, static_cast<cudaStream_t>(stream)), "bf16 decode launch");
+}
+
+// ---- block-scaled cache ----------------------------------------------------
+static i8kv_status check_block_cache(int Hkv, int D, int block_size, int num_blocks) {
+  REQUIRE(block_size == 16, I8KV_ERR_UNSUPPORTED, "block_size %d not supported (16)", block_size);
+  REQUIRE(D == 64 || D == 128 || D == 256, I8KV_ERR_UNSUPPORTED, "head_dim %d not supported (64, 128 or 256)", D);
+  REQUIRE(Hkv > 0, I8KV_ERR_INVALID_ARG, "Hkv=%d must be positive", Hkv);
+  REQUIRE(Hkv <= 256, I8KV_ERR_UNSUPPORTED, "Hkv=%d > 256 is not supported", Hkv);
+  REQUIRE(num_blocks > 0, I8KV_ERR_INVALID_ARG, "num_blocks=%d", num_blocks);
+  return I8KV_OK;
+}
+
+// Rows of a strided bf16 input: 16-byte aligned starts.
+static i8kv_status check_rows(const void* p, int64_t stride, const char* name) {
+  REQUIRE(p != nullptr, I8KV_ERR_INVALID_ARG, "%s is NULL", name);
+  REQUIRE(aligned16(p), I8KV_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  REQUIRE(stride >= 0 && stride % 8 == 0, I8KV_ERR_INVALID_ARG, "%s_stride=%lld must be a multiple of 8, not negative",
+          name, (long long)stride);
+  return I8KV_OK;
+}
+
+static i8kv_status check_ragged(int T, const int32_t* cu, const int32_t* seq_lens, const int32_t* tables, int B,
+                                int max_blocks) {
+  REQUIRE(T <= (1 << 30) && B <= (1 << 28), I8KV_ERR_UNSUPPORTED, "T=%d or B=%d too large", T, B);
+  REQUIRE(cu != nullptr || T == B, I8KV_ERR_INVALID_ARG, "T=%d rows for B=%d sequences without cu_tokens", T, B);
+  REQUIRE(seq_lens && tables, I8KV_ERR_INVALID_ARG, "null seq_lens/block_tables pointer");
+  REQUIRE(max_blocks > 0 && max_blocks <= (1 << 26), I8KV_ERR_INVALID_ARG, "max_blocks=%d", max_blocks);
+  return I8KV_OK;
+}
+
+static i8kv_status check_block_pointers(const void* k_cache, const void* v_cache, const void* k_scale,
+                                        const void* v_scale) {
+  REQUIRE(k_cache && v_cache && k_scale && v_scale, I8KV_ERR_INVALID_ARG, "null cache/scale pointer");
+  REQUIRE(aligned16(k_cache) && aligned16(v_cache) && aligned16(k_scale) && aligned16(v_scale), I8KV_ERR_INVALID_ARG,
+          "caches and scales must be 16-byte aligned");
+  return I8KV_OK;
+}
+
+#define PASS(call)                       \
+  do {                                   \
+    const i8kv_status st_ = (call);      \
+    if (st_ != I8KV_OK) return st_;      \
+  } while (0)
+
+i8kv_status i8kv_block_kv_write(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride, int T,
+                                const int32_t* cu_tokens, const int32_t* seq_lens, const int32_t* block_tables, int B,
+                                int Hkv, int D, int block_size, int max_blocks, int num_blocks, int8_t* k_cache,
+                                int8_t* v_cache, float* k_scale, float* v_scale, void* stream) {
+  REQUIRE(T >= 0 && B >= 0, I8KV_ERR_INVALID_ARG, "T=%d B=%d", T, B);
+  PASS(check_block_cache(Hkv, D, block_size, num_blocks));
+  if (T == 0 || B == 0) return I8KV_OK;
+  PASS(check_ragged(T, cu_tokens, seq_lens, block_tables, B, max_blocks));
+  PASS(check_rows(k, k_stride, "k"));
+  PASS(check_rows(v, v_stride, "v"));
+  PASS(check_block_pointers(k_cache, v_cache, k_scale, v_scale));
+  const i8kv::BlockRaggedParams r{cu_tokens, seq_lens, block_tables, T, B, Hkv, D, max_blocks, num_blocks};
+  const i8kv::BlockWriteParams p{k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale};
+  return from_cuda(i8kv::launch_block_kv_write(r, p, static_cast<cudaStream_t>(stream)), "block kv write launch");
+}
+
+i8kv_status i8kv_block_kv_read(void* k_out, void* v_out, int out_dtype, int T, const int32_t* cu_tokens,
+                               const int32_t* seq_lens, const int32_t* block_tables, int B, int Hkv, int D,
+                               int block_size, int max_blocks, int num_blocks, const int8_t* k_cache,
+                               const int8_t* v_cache, const float* k_scale, const float* v_scale, void* stream) {
+  REQUIRE(T >= 0 && B >= 0, I8KV_ERR_INVALID_ARG, "T=%d B=%d", T, B);
+  PASS(check_block_cache(Hkv, D, block_size, num_blocks));
+  if (T == 0 || B == 0) return I8KV_OK;
+  PASS(check_ragged(T, cu_tokens, seq_lens, block_tables, B, max_blocks));
+  PASS(check_out(k_out, out_dtype));
+  PASS(check_out(v_out, out_dtype));
+  PASS(check_block_pointers(k_cache, v_cache, k_scale, v_scale));
+  const i8kv::BlockRaggedParams r{cu_tokens, seq_lens, block_tables, T, B, Hkv, D, max_blocks, num_blocks};
+  const i8kv::BlockReadParams p{k_out, v_out, out_dtype == I8KV_OUT_BF16, k_cache, v_cache, k_scale, v_scale};
+  return from_cuda(i8kv::launch_block_kv_read(r, p, static_cast<cudaStream_t>(stream)), "block kv read launch");
+}
+
+// What the decode and the chunk have in common.
+static i8kv_status block_attn_common(i8kv::BlockDecodeParams& p, void* out, int out_dtype, const uint16_t* q,
+                                     int64_t q_stride, const int8_t* k_cache, const int8_t* v_cache,
+                                     const float* k_scale, const float* v_scale, const float* alibi_slopes, int Hq,
+                                     int Hkv, int D, int num_blocks, float softmax_scale, float softcap, int window) {
+  PASS(check_out(out, out_dtype));
+  PASS(check_rows(q, q_stride, "q"));
+  PASS(check_block_pointers(k_cache, v_cache, k_scale, v_scale));
+  p.out = out;
+  p.out_bf16 = out_dtype == I8KV_OUT_BF16;
+  p.q = q;
+  p.q_stride = q_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.slopes = alibi_slopes;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.D = D;
+  p.num_blocks = num_blocks;
+  p.window = window;
+  const float log2e = 1.4426950408889634f;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)D);
+  p.score_mul = softcap > 0.f ? scale * log2e * (2.0f / softcap) : scale * log2e;
+  p.cap_log2 = softcap > 0.f ? softcap * log2e : 0.f;
+  return I8KV_OK;
+}
+
+static i8kv_status check_block_attn(int Hq, int Hkv, int D, int block_size, int num_blocks, float softcap, int window) {
+  PASS(check_block_cache(Hkv, D, block_size, num_blocks));
+  REQUIRE(Hq > 0 && Hq % Hkv == 0, I8KV_ERR_INVALID_ARG, "Hq=%d is not a positive multiple of Hkv=%d", Hq, Hkv);
+  REQUIRE(Hq <= 4096, I8KV_ERR_UNSUPPORTED, "Hq=%d > 4096 is not supported", Hq);
+  REQUIRE(softcap == 0.f || (softcap >= 1e-3f && softcap <= 1e4f), I8KV_ERR_INVALID_ARG,
+          "softcap must be 0 (none) or in [1e-3, 1e4]");
+  REQUIRE(window >= 0, I8KV_ERR_INVALID_ARG, "window=%d < 0 (0: none)", window);
+  return I8KV_OK;
+}
+
+static int head_passes(int Hq, int Hkv) { return (Hq / Hkv + 7) / 8; }
+
+size_t i8kv_block_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks) {
+  if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || max_blocks <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
+  return i8kv::block_decode_workspace_bytes(D, i8kv::block_decode_grid(B, Hkv * head_passes(Hq, Hkv), max_blocks));
+}
+
+i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
+                                   const int8_t* v_cache, const float* k_scale, const float* v_scale,
+                                   const int32_t* block_tables, const int32_t* seq_lens, const int32_t* key_begin,
+                                   const float* alibi_slopes, int B, int Hq, int Hkv, int D, int block_size,
+                                   int max_blocks, int num_blocks, float softmax_scale, float softcap, int window,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  REQUIRE(B >= 0, I8KV_ERR_INVALID_ARG, "B=%d < 0", B);
+  PASS(check_block_attn(Hq, Hkv, D, block_size, num_blocks, softcap, window));
+  if (B == 0) return I8KV_OK;
+  PASS(check_ragged(B, nullptr, seq_lens, block_tables, B, max_blocks));
+  i8kv::BlockDecodeParams p{};
+  PASS(block_attn_common(p, out, out_dtype, q, q_stride, k_cache, v_cache, k_scale, v_scale, alibi_slopes, Hq, Hkv, D,
+                         num_blocks, softmax_scale, softcap, window));
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.key_begin = key_begin;
+  p.B = B;
+  p.max_blocks = max_blocks;
+  p.HG = head_passes(Hq, Hkv);
+  p.HH = Hkv * p.HG;
+  p.grid = i8kv::block_decode_grid(B, p.HH, max_blocks);
+  const size_t need = i8kv::block_decode_workspace_bytes(D, p.grid);
+  REQUIRE(workspace != nullptr && workspace_bytes >= need, I8KV_ERR_WORKSPACE,
+          "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  REQUIRE(aligned16(workspace), I8KV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  p.ws = workspace;
+  return from_cuda(i8kv::launch_block_decode(p, static_cast<cudaStream_t>(stream)), "block decode launch");
+}
+
+// Row groups of a chunk (8 (token, head) rows each).
+static int chunk_groups(int C, int Hq, int Hkv) { return (int)(((int64_t)C * (Hq / Hkv) + 7) / 8); }
+
+size_t i8kv_block_prefix_workspace_bytes(int history_len, int chunk_len, int Hq, int Hkv, int D) {
+  if (history_len < 0 || chunk_len <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
+  if ((int64_t)history_len + chunk_len > (1 << 30)) return 0;
+  const int blocks = (history_len + chunk_len + 15) / 16;
+  return i8kv::block_decode_workspace_bytes(D, i8kv::block_decode_grid(chunk_groups(chunk_len, Hq, Hkv), Hkv, blocks));
+}
+
+i8kv_status i8kv_block_prefix_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
+                                   const int8_t* v_cache, const float* k_scale, const float* v_scale,
+                                   const int32_t* block_table, int history_len, int chunk_len, const int32_t* key_begin,
+                                   const int32_t* key_end, const float* alibi_slopes, int Hq, int Hkv, int D,
+                                   int block_size, int num_blocks, float softmax_scale, float softcap, int window,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  REQUIRE(history_len >= 0 && chunk_len >= 0, I8KV_ERR_INVALID_ARG, "history_len=%d chunk_len=%d", history_len,
+          chunk_len);
+  REQUIRE((int64_t)history_len + chunk_len <= (1 << 30), I8KV_ERR_UNSUPPORTED, "history_len + chunk_len > 2^30");
+  PASS(check_block_attn(Hq, Hkv, D, block_size, num_blocks, softcap, window));
+  if (chunk_len == 0) return I8KV_OK;
+  REQUIRE((int64_t)chunk_len * (Hq / Hkv) <= (1 << 30), I8KV_ERR_UNSUPPORTED, "chunk_len * Hq / Hkv > 2^30");
+  REQUIRE(block_table != nullptr, I8KV_ERR_INVALID_ARG, "block_table is NULL");
+  i8kv::BlockDecodeParams p{};
+  PASS(block_attn_common(p, out, out_dtype, q, q_stride, k_cache, v_cache, k_scale, v_scale, alibi_slopes, Hq, Hkv, D,
+                         num_blocks, softmax_scale, softcap, window));
+  p.block_tables = block_table;
+  p.key_begin = key_begin;
+  p.key_end = key_end;
+  p.H = history_len;
+  p.C = chunk_len;
+  p.B = chunk_groups(chunk_len, Hq, Hkv);
+  p.max_blocks = (history_len + chunk_len + 15) / 16;
+  p.HG = 1;
+  p.HH = Hkv;
+  p.grid = i8kv::block_decode_grid(p.B, p.HH, p.max_blocks);
+  const size_t need = i8kv::block_decode_workspace_bytes(D, p.grid);
+  REQUIRE(workspace != nullptr && workspace_bytes >= need, I8KV_ERR_WORKSPACE,
+          "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+  REQUIRE(aligned16(workspace), I8KV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  p.ws = workspace;
+  return from_cuda(i8kv::launch_block_chunk_rows(p, static_cast<cudaStream_t>(stream)), "block chunk launch");
 }
 
 }  // extern "C"

@@ -108,10 +108,64 @@ struct PrefixParams {
   const uint16_t* vb_cache;  // [NB, Hkv, D, 16]
 };
 
+// Block-scaled cache: one fp32 scale per (16-token block, KV head).  A ragged
+// call covers, for every sequence b, its last cu[b + 1] - cu[b] positions (one
+// when cu is NULL, and T = B); they are rows cu[b] .. cu[b + 1] - 1 of the call.
+struct BlockRaggedParams {
+  const int32_t* cu;            // [B + 1], nullable
+  const int32_t* seq_lens;      // [B], the covered positions included
+  const int32_t* block_tables;  // [B, max_blocks]
+  int T, B, Hkv, D, max_blocks, num_blocks;
+};
+struct BlockWriteParams {
+  const uint16_t* k;  // bf16 rows [T] of [Hkv, D], k_stride elements apart
+  const uint16_t* v;
+  int64_t k_stride, v_stride;
+  int8_t* k_cache;
+  int8_t* v_cache;
+  float* k_scale;  // [NB, Hkv]
+  float* v_scale;
+};
+struct BlockReadParams {
+  void* k_out;  // [T, Hkv, D], fp32 or bf16
+  void* v_out;
+  int out_bf16;
+  const int8_t* k_cache;
+  const int8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+};
+struct BlockDecodeParams {
+  void* out;  // [B, Hq, D]
+  int out_bf16;
+  const uint16_t* q;  // bf16 rows [B] of [Hq, D], q_stride elements apart
+  int64_t q_stride;
+  const int8_t* k_cache;
+  const int8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* key_begin;  // [B] or [C], nullable: the first visible key
+  const float* slopes;       // [Hq], nullable
+  int B, Hq, Hkv, G, D, max_blocks, num_blocks, window;
+  int HG, HH;       // passes of 8 query heads per KV head; Hkv * HG
+  // A chunk of one sequence (rows (token, head) of one KV head in groups of 8):
+  // B = ceil(C G / 8) groups, HH = Hkv, block_tables one row, seq_lens unused.
+  int H, C;
+  const int32_t* key_end;    // [C], nullable: one past the last visible key
+  float score_mul;  // q . k -> log2 units (no cap) or twice the tanh's argument in log2 units
+  float cap_log2;   // the cap in log2 units, 0: none
+  void* ws;
+  int grid;
+};
+
 // Per-translation-unit device error words (read and cleared).
 cudaError_t read_error_producer(int* value);
 cudaError_t read_error_decode(int* value);
 cudaError_t read_error_prefix(int* value);
+cudaError_t read_error_block_cache(int* value);
+cudaError_t read_error_block_decode(int* value);
 
 cudaError_t launch_kv_quant_write(const ProducerParams& p, cudaStream_t stream);
 cudaError_t launch_kv_rope_quant_write(const ProducerParams& p, cudaStream_t stream);
@@ -133,5 +187,12 @@ cudaError_t noalloc_scratch_address(void** addr);
 cudaError_t launch_int8_prefix(const PrefixParams& p, cudaStream_t stream);
 cudaError_t launch_bf16_prefix(const PrefixParams& p, cudaStream_t stream);
 cudaError_t launch_debug_prefix(const PrefixParams& p, cudaStream_t stream);
+
+cudaError_t launch_block_kv_write(const BlockRaggedParams& r, const BlockWriteParams& p, cudaStream_t stream);
+cudaError_t launch_block_kv_read(const BlockRaggedParams& r, const BlockReadParams& p, cudaStream_t stream);
+int block_decode_grid(int entries, int HH, int max_blocks);
+size_t block_decode_workspace_bytes(int D, int grid);
+cudaError_t launch_block_decode(const BlockDecodeParams& p, cudaStream_t stream);
+cudaError_t launch_block_chunk_rows(const BlockDecodeParams& p, cudaStream_t stream);
 
 }  // namespace i8kv
