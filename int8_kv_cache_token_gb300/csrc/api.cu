@@ -72,7 +72,9 @@ i8kv_status i8kv_device_error(int* code) {
   if (e != cudaSuccess) return from_cuda(e, "i8kv_device_error: synchronize");
   int v = 0;
   cudaError_t (*readers[])(int*) = {i8kv::read_error_producer, i8kv::read_error_decode, i8kv::read_error_prefix,
-                                    i8kv::read_error_block_cache, i8kv::read_error_block_decode};
+                                    i8kv::read_error_block_cache, i8kv::read_error_block_decode,
+                                    i8kv::read_error_block_prefix_64, i8kv::read_error_block_prefix_128,
+                                    i8kv::read_error_block_prefix_256};
   for (auto rd : readers) {
     int x = 0;
     e = rd(&x);
@@ -679,14 +681,10 @@ i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, 
   return from_cuda(i8kv::launch_block_decode(p, static_cast<cudaStream_t>(stream)), "block decode launch");
 }
 
-// Row groups of a chunk (8 (token, head) rows each).
-static int chunk_groups(int C, int Hq, int Hkv) { return (int)(((int64_t)C * (Hq / Hkv) + 7) / 8); }
-
 size_t i8kv_block_prefix_workspace_bytes(int history_len, int chunk_len, int Hq, int Hkv, int D) {
   if (history_len < 0 || chunk_len <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || (D != 64 && D != 128 && D != 256)) return 0;
-  if ((int64_t)history_len + chunk_len > (1 << 30)) return 0;
-  const int blocks = (history_len + chunk_len + 15) / 16;
-  return i8kv::block_decode_workspace_bytes(D, i8kv::block_decode_grid(chunk_groups(chunk_len, Hq, Hkv), Hkv, blocks));
+  if ((int64_t)history_len + chunk_len > (1 << 30) || (int64_t)chunk_len * (Hq / Hkv) > (1 << 30)) return 0;
+  return i8kv::block_prefix_workspace_bytes(history_len, chunk_len, Hq / Hkv, Hkv, D);
 }
 
 i8kv_status i8kv_block_prefix_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
@@ -700,7 +698,11 @@ i8kv_status i8kv_block_prefix_attn(void* out, int out_dtype, const uint16_t* q, 
   REQUIRE((int64_t)history_len + chunk_len <= (1 << 30), I8KV_ERR_UNSUPPORTED, "history_len + chunk_len > 2^30");
   PASS(check_block_attn(Hq, Hkv, D, block_size, num_blocks, softcap, window));
   if (chunk_len == 0) return I8KV_OK;
-  REQUIRE((int64_t)chunk_len * (Hq / Hkv) <= (1 << 30), I8KV_ERR_UNSUPPORTED, "chunk_len * Hq / Hkv > 2^30");
+  // the work list: (KV head, 128-row block, 128-key tile) steps, counted in 32 bits
+  REQUIRE((int64_t)chunk_len * (Hq / Hkv) <= (1 << 30) &&
+              (((int64_t)chunk_len * (Hq / Hkv) + 127) / 128) * Hkv * (((int64_t)history_len + chunk_len) / 128 + 1) < (1ll << 31),
+          I8KV_ERR_UNSUPPORTED, "chunk_len=%d rows over %lld keys are too many for one call", chunk_len,
+          (long long)history_len + chunk_len);
   REQUIRE(block_table != nullptr, I8KV_ERR_INVALID_ARG, "block_table is NULL");
   i8kv::BlockDecodeParams p{};
   PASS(block_attn_common(p, out, out_dtype, q, q_stride, k_cache, v_cache, k_scale, v_scale, alibi_slopes, Hq, Hkv, D,
@@ -710,17 +712,12 @@ i8kv_status i8kv_block_prefix_attn(void* out, int out_dtype, const uint16_t* q, 
   p.key_end = key_end;
   p.H = history_len;
   p.C = chunk_len;
-  p.B = chunk_groups(chunk_len, Hq, Hkv);
-  p.max_blocks = (history_len + chunk_len + 15) / 16;
-  p.HG = 1;
-  p.HH = Hkv;
-  p.grid = i8kv::block_decode_grid(p.B, p.HH, p.max_blocks);
-  const size_t need = i8kv::block_decode_workspace_bytes(D, p.grid);
+  const size_t need = i8kv::block_prefix_workspace_bytes(history_len, chunk_len, p.G, Hkv, D);
   REQUIRE(workspace != nullptr && workspace_bytes >= need, I8KV_ERR_WORKSPACE,
           "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
   REQUIRE(aligned16(workspace), I8KV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   p.ws = workspace;
-  return from_cuda(i8kv::launch_block_chunk_rows(p, static_cast<cudaStream_t>(stream)), "block chunk launch");
+  return from_cuda(i8kv::launch_block_prefix(p, static_cast<cudaStream_t>(stream)), "block chunk launch");
 }
 
 }  // extern "C"

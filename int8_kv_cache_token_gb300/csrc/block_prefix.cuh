@@ -1,0 +1,831 @@
+// block_prefix.cuh -- chunk attention over the block-scaled INT8 KV cache on the
+// 5th-generation tensor cores (the kernels; one .cu per head_dim instantiates them).
+//
+// Row (token j, query head h) at position pos = H + j over its visible keys:
+//   x_t = scale q . (sK cK_t),  s_t = cap tanh(x_t / cap) (or x_t) - slope_h |pos - t|
+//   O = sum_t softmax(s)_t sV cV_t
+// as in block_decode.cu: u_t = s_t log2 e + log2 sV, weights w_t = 2^(u_t - M),
+// O = sum w cV / sum w / sV, so the two scales of a 16-key block are one multiply
+// and one addend of its 16 scores, and the products below run on the bare codes.
+//
+// A CTA owns 128 rows (token, head) of one KV head at a time and walks 128-key
+// tiles:
+//   S = Q K^T    tcgen05, bf16 Q (as given) x bf16 codes (exact), M = N = 128, K = D
+//   u, M, w      CUDA cores, one thread per row
+//   O += W V     tcgen05, f16 W (from tensor memory) x f16 codes (exact), N = D
+// S has two slots in tensor memory, so the softmax of one tile runs beside the
+// products of its neighbours; two warpgroups take alternate tiles and hand the
+// running maximum on.  W overwrites its S slot.  O stays in tensor memory and is
+// rescaled only when a row's maximum grows by more than 2^8.  For an fp32 output W
+// is two f16 parts (2^-22 instead of 2^-12 relative), side by side in the slot.
+//
+// The codes become 16-bit operand tiles once per call (block_tiles_kernel), in
+// the swizzled layout that the MMAs read, so a tile is one bulk copy per half and
+// every row block of a KV head shares the conversion.
+//
+// All (KV head, row block, tile) steps form one list, cut evenly over one CTA per
+// SM; row blocks that span CTAs leave (O, M, l) records, merged in CTA order by a
+// third kernel.  So a causal triangle, a window, packed documents and a short
+// chunk over a long history all fill the GPU.
+//
+// Warps: 0 tile copies (one lane), 1 MMA issue (one lane), 2 tensor memory, 4-7
+// and 8-11 softmax.  One thread issues both products: MMAs of a CTA execute in
+// issue order, which is what lets W share its S slot with the S after next.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace i8kv {
+namespace bp {
+
+constexpr int kBS = 16;
+constexpr int kRows = 128;
+constexpr int kKeys = 128;
+constexpr int kBlk = kKeys / kBS;  // cache blocks per tile
+constexpr int kThreads = 384;
+constexpr int kWG = 128;
+constexpr int kSoftWarp = 4;
+constexpr float kLazy = 8.0f;
+// Registers: 128 control threads at 56, 256 softmax threads at 224 (128 scores
+// each); 56 + 2 x 224 = 3 x 168, what 384 threads launch with.
+constexpr int kRegsCtl = 56, kRegsSoft = 224;
+static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * 168, "register split");
+constexpr int kScales = 3 * kBlk;  // per tile: sK, log2 sV, 1 / sV of its blocks
+
+// The workspace (all offsets multiples of 128 bytes).
+struct Head {
+  int rb, kvh, first, cnt;  // where a CTA's range starts: row block (-1: empty range), KV head, tile, tiles
+  int total, pad[3];
+};
+static_assert(sizeof(Head) == 32, "");
+struct Range {
+  int lo, hi;        // the row block's tiles
+  int lo_in, hi_in;  // keys that every row of it sees
+};
+struct Plan {
+  int nrb, tile0, ntiles, grid;
+  size_t oHead, oRange, oScale, oK, oV, oRec, bytes;
+};
+inline Plan plan_of(int H, int C, int G, int Hkv, int D, int window, int grid) {
+  Plan p;
+  auto up = [](size_t x) { return (x + 127) / 128 * 128; };
+  p.nrb = (int)(((int64_t)C * G + kRows - 1) / kRows);
+  p.tile0 = window > 0 && H - window + 1 > 0 ? (H - window + 1) / kKeys : 0;  // no row sees an earlier key
+  p.ntiles = (H + C + kKeys - 1) / kKeys - p.tile0;
+  p.grid = grid;
+  const size_t tile = (size_t)kKeys * D * 2, n = (size_t)p.ntiles * Hkv;
+  p.oHead = 0;
+  p.oRange = up(sizeof(Head) * grid);
+  p.oScale = p.oRange + up(sizeof(Range) * (size_t)p.nrb);
+  p.oK = p.oScale + up(n * kScales * 4);
+  p.oV = p.oK + n * tile;
+  p.oRec = p.oV + n * tile;
+  p.bytes = p.oRec + (size_t)2 * grid * kRows * (D + 2) * 4;
+  return p;
+}
+
+struct Params {
+  BlockDecodeParams a;
+  Plan w;
+};
+
+template <int D>
+struct Lay {
+  static constexpr int kParts = D == 64 ? 1 : 2;       // stages per operand tile
+  static constexpr int kTile = kKeys * D * 2;
+  static constexpr int kStage = kTile / kParts;        // K: half the dims; V: half the keys
+  static constexpr int kStages = D == 256 ? 5 : 12;
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int oQ = 0;                         // [D/64][128 rows][128 B], then the row statistics
+  static constexpr int oRing = oQ + kQ;
+  static constexpr int oM = oRing + kStages * kStage;  // M [2][128]
+  static constexpr int oSc = oM + 2 * kRows * 4;       // scales of 8 tiles
+  static constexpr int oBar = oSc + 8 * kScales * 4;
+  // full[kStages], free[kStages], sc_full[8], s_full[2], p_full[2], m_full[2], pv_done[2], q_full, o_free
+  static constexpr int kBars = 2 * kStages + 8 + 2 + 2 + 2 + 2 + 2;
+  static constexpr int oCtl = oBar + kBars * 8;
+  static constexpr int kTotal = oCtl + 16;
+  static_assert(kTotal <= 232448, "shared memory");
+  static constexpr uint32_t kOCol = 256;
+};
+
+// Byte offset of 16-byte chunk c of row r of a 128-byte-row tile, swizzled.
+__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ void interval(const BlockDecodeParams& p, int j, int& lo, int& hi) {
+  lo = 0;
+  if (p.window > 0) lo = max(0, p.H + j - p.window + 1);
+  if (p.key_begin != nullptr) lo = max(lo, p.key_begin[j]);
+  hi = p.H + j + 1;
+  if (p.key_end != nullptr) hi = min(p.key_end[j], p.H + p.C);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_codes(uint32_t w, int i) {
+  return bf16x2_rn((float)(int8_t)((w >> (8 * i)) & 0xffu), (float)(int8_t)((w >> (8 * i + 8)) & 0xffu));
+}
+
+// ---- operand tiles and scales: one CTA per (tile, KV head); also the row blocks'
+// tile ranges, spread over the CTAs' warps.
+template <int D>
+__global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant__ Params pp) {
+  const BlockDecodeParams& p = pp.a;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = blockIdx.x, kvh = blockIdx.y;
+  uint8_t* ws = static_cast<uint8_t*>(p.ws);
+  // row block ranges
+  for (int rb = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; rb < pp.w.nrb; rb += gridDim.x * gridDim.y * 8) {
+    const int j0 = (int)((int64_t)rb * kRows / p.G), j1 = min(p.C - 1, (int)(((int64_t)rb * kRows + kRows - 1) / p.G));
+    int lo = 0x7fffffff, hi = 0, lo_in = 0, hi_in = 0x7fffffff;
+    for (int j = j0 + lane; j <= j1; j += 32) {
+      int a, b;
+      interval(p, j, a, b);
+      lo_in = max(lo_in, a);
+      hi_in = min(hi_in, b);
+      if (a < b) {
+        lo = min(lo, a);
+        hi = max(hi, b);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo_in = __reduce_max_sync(0xffffffffu, lo_in);
+    hi_in = __reduce_min_sync(0xffffffffu, hi_in);
+    if (lane == 0) {
+      Range r;
+      r.lo = lo < hi ? lo / kKeys : 0;
+      r.hi = lo < hi ? (hi + kKeys - 1) / kKeys : 0;
+      r.lo_in = lo_in;
+      r.hi_in = hi_in;
+      reinterpret_cast<Range*>(ws + pp.w.oRange)[rb] = r;
+    }
+  }
+  const int n = p.H + p.C;
+  const int blk0 = (pp.w.tile0 + tile) * kBlk;
+  int phys[kBlk];
+#pragma unroll
+  for (int i = 0; i < kBlk; ++i) {
+    phys[i] = -1;
+    if ((blk0 + i) * kBS < n) {
+      const int b = __ldg(p.block_tables + blk0 + i);
+      phys[i] = b >= 0 && b < p.num_blocks ? b : -2;  // -2: no such block; an error for a row that sees it
+    }
+  }
+  const size_t ti = (size_t)kvh * pp.w.ntiles + tile;
+  uint8_t* kt = ws + pp.w.oK + ti * Lay<D>::kTile;
+  uint8_t* vt = ws + pp.w.oV + ti * Lay<D>::kTile;
+  if (tid < kBlk) {
+    float sk = 0.f, sv = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kBlk; ++i)
+      if (i == tid) {
+        bad = phys[i] == -2;
+        if (phys[i] >= 0) {
+          sk = p.k_scale[(size_t)phys[i] * p.Hkv + kvh] * p.score_mul;
+          sv = p.v_scale[(size_t)phys[i] * p.Hkv + kvh];
+        }
+      }
+    sv = fmaxf(sv, kTinyDivisor);
+    float* s = reinterpret_cast<float*>(ws + pp.w.oScale) + ti * kScales;
+    s[tid] = sk;
+    s[kBlk + tid] = bad ? 0.f : log2f(sv);
+    s[2 * kBlk + tid] = bad ? -1.f : __frcp_rn(sv);
+  }
+  // K page [D/16][16 tokens][16 B] and V page [D][16 B]: D chunks each per block.
+  // D = 256: a thread per chunk; below, 256 / D blocks at once.
+  constexpr int kAt = 256 / D;
+  const int sub = tid / D, c = tid % D;
+#pragma unroll
+  for (int i0 = 0; i0 < kBlk; i0 += 4 * kAt) {
+    uint4 kx[4], vx[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      int ph = -1;
+#pragma unroll
+      for (int s = 0; s < kAt; ++s)
+        if (i0 + u * kAt + s < kBlk && s == sub) ph = phys[(i0 + u * kAt + s) % kBlk];
+      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
+      if (ph >= 0) {
+        const size_t page = ((size_t)ph * p.Hkv + kvh) * (D * kBS);
+        kx[u] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + page) + c);
+        vx[u] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + page) + c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kAt + sub;
+      if (i >= kBlk) continue;
+      const int dc = c / kBS, key = i * kBS + c % kBS;
+      uint8_t* atom = kt + (size_t)(dc / 4) * (kKeys * 128);
+      *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4))) =
+          make_uint4(bf16x2_codes(kx[u].x, 0), bf16x2_codes(kx[u].x, 2), bf16x2_codes(kx[u].y, 0), bf16x2_codes(kx[u].y, 2));
+      *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4) + 1)) =
+          make_uint4(bf16x2_codes(kx[u].z, 0), bf16x2_codes(kx[u].z, 2), bf16x2_codes(kx[u].w, 0), bf16x2_codes(kx[u].w, 2));
+      uint8_t* half = vt + (size_t)(i / 4) * (D * 128);
+      uint4 h0, h1;
+      s8x4_to_f16(vx[u].x, h0.x, h0.y);
+      s8x4_to_f16(vx[u].y, h0.z, h0.w);
+      s8x4_to_f16(vx[u].z, h1.x, h1.y);
+      s8x4_to_f16(vx[u].w, h1.z, h1.w);
+      *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4))) = h0;
+      *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4) + 1)) = h1;
+    }
+  }
+}
+
+// ---- the walk over a CTA's range of the list (KV head, row block, tile)
+struct Walk {
+  int kvh, rb, first, len, left, cnt, lo;  // segment: tiles lo + first .. + len of the row block
+};
+__device__ __forceinline__ void walk_load(const Range* rg, Walk& w) {
+  w.lo = rg[w.rb].lo;
+  w.cnt = rg[w.rb].hi - w.lo;
+  w.len = min(w.cnt - w.first, w.left);
+}
+__device__ __forceinline__ bool walk_next(const Params& pp, const Range* rg, Walk& w) {
+  w.left -= w.len;
+  if (w.left <= 0) return false;
+  w.first = 0;
+  do {
+    if (++w.rb == pp.w.nrb) {
+      w.rb = 0;
+      if (++w.kvh == pp.a.Hkv) return false;
+    }
+    walk_load(rg, w);
+  } while (w.cnt == 0);
+  return true;
+}
+
+// The cut of `total` steps over `grid` CTAs: the first total % grid take one more.
+__host__ __device__ __forceinline__ int cut_at(int total, int grid, int c) { return total / grid * c + min(c, total % grid); }
+__device__ __forceinline__ int cta_of(int total, int grid, int u) {
+  const int per = total / grid, rem = total % grid, big = rem * (per + 1);
+  return u < big ? u / (per + 1) : rem + (u - big) / per;
+}
+
+// Bounded wait that gives up at once when the CTA has aborted (error 1 after the
+// time limit); every thread still runs its loops and barriers.
+__device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (*abort_flag) return;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort_flag) return;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      record_error(1);
+      *abort_flag = 1;
+      return;
+    }
+  }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The part of (a, b) that their packed f16 `hi` leaves over, as f16x2.
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t hi, float a, float b) {
+  float fa, fb;
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(fa), "=f"(fb) : "r"(hi));
+  return f16x2_of(a - fa, b - fb);
+}
+
+template <int D, bool kCap, bool kSlope, bool kHiLo>
+__global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_constant__ Params pp) {
+  using Ly = Lay<D>;
+  constexpr int NS = Ly::kStages;
+  const BlockDecodeParams& p = pp.a;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::oBar);
+  uint64_t* free_ = full + NS;
+  uint64_t* sc_full = free_ + NS;   // [n % 8] scales of tile n
+  uint64_t* s_full = sc_full + 8;   // [n & 1] S of tile n in tensor memory
+  uint64_t* p_full = s_full + 2;    // [n & 1] W of tile n in tensor memory
+  uint64_t* m_full = p_full + 2;    // [n & 1] the running maxima after tile n
+  uint64_t* pv_done = m_full + 2;   // [n & 1] the product of tile n has joined O
+  uint64_t* q_full = pv_done + 2;   // the segment's query rows in shared memory
+  uint64_t* o_free = q_full + 1;    // the segment's O is read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::oCtl);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::oCtl + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* ws = static_cast<uint8_t*>(p.ws);
+  const Range* rg = reinterpret_cast<const Range*>(ws + pp.w.oRange);
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&free_[i], 1);
+    }
+    for (int i = 0; i < 8; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kWG);
+      mbar_init(&m_full[i], kWG);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, 2 * kWG);
+    mbar_init(o_free, 2 * kWG);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- this CTA's range of the list ----
+  int* scan = reinterpret_cast<int*>(smem + Ly::oQ);  // [12] warp sums, [16 ..] the start
+  const int grid = gridDim.x;
+  auto scan_step = [&](int v, int& before) {
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int base = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) base += scan[i];
+      sum += scan[i];
+    }
+    before = base + x - v;
+    return sum;
+  };
+  int per_head = 0, before;
+  for (int r0 = 0; r0 < pp.w.nrb; r0 += kThreads) {
+    const int rb = r0 + tid;
+    per_head += scan_step(rb < pp.w.nrb ? rg[rb].hi - rg[rb].lo : 0, before);
+  }
+  const int total = per_head * p.Hkv;
+  const int u0 = cut_at(total, grid, blockIdx.x), u1 = cut_at(total, grid, blockIdx.x + 1);
+  if (tid < 2) scan[16 + tid] = 0;
+  const int kvh0 = per_head > 0 ? u0 / per_head : 0;
+  {
+    int run = kvh0 * per_head;
+    for (int r0 = 0; r0 < pp.w.nrb; r0 += kThreads) {
+      const int rb = r0 + tid;
+      const int cnt = rb < pp.w.nrb ? rg[rb].hi - rg[rb].lo : 0;
+      const int sum = scan_step(cnt, before);
+      const int s0 = run + before;
+      if (u0 >= s0 && u0 < s0 + cnt) {
+        scan[16] = rb;
+        scan[17] = u0 - s0;
+      }
+      run += sum;
+    }
+  }
+  __syncthreads();
+  Walk w;
+  w.kvh = kvh0;
+  w.rb = scan[16];
+  w.first = scan[17];
+  w.left = u1 - u0;
+  walk_load(rg, w);
+  if (tid == 0) {
+    Head h{};
+    h.rb = u0 < u1 ? w.rb : -1;
+    h.kvh = w.kvh;
+    h.first = w.first;
+    h.cnt = w.cnt;
+    h.total = total;
+    reinterpret_cast<Head*>(ws + pp.w.oHead)[blockIdx.x] = h;
+  }
+  // row blocks without a visible key: zero rows
+  for (int rb = blockIdx.x; rb < pp.w.nrb; rb += grid) {
+    if (rg[rb].hi != rg[rb].lo) continue;
+    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
+      const int64_t r = (int64_t)rb * kRows + i / (D / 4);
+      if (r < (int64_t)p.C * p.G)
+        for (int k = 0; k < p.Hkv; ++k)
+          store_out4(p.out, p.out_bf16, ((size_t)(r / p.G) * p.Hq + k * p.G + r % p.G) * D + (i % (D / 4)) * 4,
+                     make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
+  __syncthreads();  // the scan buffer (the query tile) is free
+
+  if (warp < kSoftWarp) {
+    regs_dec<kRegsCtl>();
+    if (u0 < u1 && warp == 0 && lane == 0) {
+      // ================= tile copies =================
+      int c = 0, n = 0;  // stages filled, tiles of K
+      const uint8_t* src[2] = {ws + pp.w.oK, ws + pp.w.oV};
+      const float* scl = reinterpret_cast<const float*>(ws + pp.w.oScale);
+      auto load = [&](int which, size_t ti) {
+#pragma unroll
+        for (int h = 0; h < Ly::kParts; ++h, ++c) {
+          const int st = c % NS;
+          if (c >= NS) pwait(&free_[st], ((c / NS) - 1) & 1, abort_flag);
+          if (*abort_flag) return;
+          mbar_expect_tx(&full[st], Ly::kStage);
+          bulk_g2s(smem + Ly::oRing + st * Ly::kStage, src[which] + ti * Ly::kTile + h * Ly::kStage, Ly::kStage, &full[st]);
+          mbar_arrive(&full[st]);
+        }
+        if (which == 0) {
+          uint64_t* b = &sc_full[n % 8];
+          mbar_expect_tx(b, kScales * 4);
+          bulk_g2s(smem + Ly::oSc + (n % 8) * kScales * 4, scl + ti * kScales, kScales * 4, b);
+          mbar_arrive(b);
+          ++n;
+        }
+      };
+      do {
+        const size_t t0 = (size_t)w.kvh * pp.w.ntiles + (w.lo + w.first - pp.w.tile0);
+        load(0, t0);
+        for (int t = 0; t < w.len && !*abort_flag; ++t) {
+          if (t + 1 < w.len) load(0, t0 + t + 1);
+          load(1, t0 + t);
+        }
+      } while (!*abort_flag && walk_next(pp, rg, w));
+      if (*abort_flag) {  // copies under way land before the CTA exits
+        for (int k = max(0, c - NS); k < c; ++k) mbar_wait(&full[k % NS], (k / NS) & 1);
+        for (int k = max(0, n - 8); k < n; ++k) mbar_wait(&sc_full[k % 8], (k / 8) & 1);
+      }
+    } else if (u0 < u1 && warp == 1 && lane == 0) {
+      // ================= MMA issue =================
+      constexpr uint32_t idesc_qk = umma_idesc_bf16(kRows, kKeys);
+      constexpr uint32_t idesc_pv = umma_idesc_f16(kRows, D);
+      const uint32_t q0 = smem_u32(smem + Ly::oQ), ring = smem_u32(smem + Ly::oRing);
+      int c = 0, n = 0, seg = 0;
+      uint64_t* last = nullptr;
+      uint32_t last_par = 0;
+      auto qk = [&](int m) {  // S of the CTA's tile m
+#pragma unroll
+        for (int h = 0; h < Ly::kParts; ++h, ++c) {
+          const int st = c % NS;
+          pwait(&full[st], (c / NS) & 1, abort_flag);
+          tc_fence_after();
+          constexpr int kSteps = D / 16 / Ly::kParts;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int kk = h * kSteps + k;
+            umma_f16(tmem + (m & 1) * kKeys, umma_desc(q0 + (kk / 4) * (kRows * 128) + (kk % 4) * 32, 128),
+                     umma_desc(ring + st * Ly::kStage + (k / 4) * (kKeys * 128) + (k % 4) * 32, 128), idesc_qk, kk > 0);
+          }
+          umma_commit(&free_[st]);
+        }
+        umma_commit(&s_full[m & 1]);
+        last = &s_full[m & 1];
+        last_par = (m >> 1) & 1;
+      };
+      do {
+        pwait(q_full, seg & 1, abort_flag);
+        qk(n);
+        for (int t = 0; t < w.len && !*abort_flag; ++t, ++n) {
+          if (t + 1 < w.len) qk(n + 1);
+          pwait(&p_full[n & 1], (n >> 1) & 1, abort_flag);
+          if (t == 0 && seg > 0) pwait(o_free, (seg - 1) & 1, abort_flag);
+          if (*abort_flag) break;
+#pragma unroll
+          for (int h = 0; h < Ly::kParts; ++h, ++c) {
+            const int st = c % NS;
+            pwait(&full[st], (c / NS) & 1, abort_flag);
+            tc_fence_after();
+            constexpr int kSteps = kKeys / 16 / Ly::kParts;
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+              const int kk = h * kSteps + k;
+              const uint64_t vd = umma_desc(ring + st * Ly::kStage + (k / 4) * (D * 128) + (k % 4) * 32, 128);
+              umma_f16_ta(tmem + Ly::kOCol, tmem + (n & 1) * kKeys + kk * 8, vd, idesc_pv, t > 0 || kk > 0);
+              if constexpr (kHiLo) umma_f16_ta(tmem + Ly::kOCol, tmem + (n & 1) * kKeys + 64 + kk * 8, vd, idesc_pv, true);
+            }
+            umma_commit(&free_[st]);
+          }
+          umma_commit(&pv_done[n & 1]);
+          last = &pv_done[n & 1];
+          last_par = (n >> 1) & 1;
+        }
+        ++seg;
+      } while (!*abort_flag && walk_next(pp, rg, w));
+      if (last) mbar_wait(last, last_par);  // every MMA has completed before tensor memory is released
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax: a thread per row, the warpgroups on alternate tiles =================
+    regs_inc<kRegsSoft>();
+    const int wg = (warp - kSoftWarp) >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    float* mref = reinterpret_cast<float*>(smem + Ly::oM);
+    float* stat = reinterpret_cast<float*>(smem + Ly::oQ);  // [wg][l, M][128], once the query tile is read
+    const int64_t R = (int64_t)p.C * p.G;
+    int n = 0;
+    bool first_seg = true;
+    if (u0 < u1) do {
+      const int64_t r = (int64_t)w.rb * kRows + row;
+      const bool valid = r < R;
+      const int j = valid ? (int)(r / p.G) : 0, hq = w.kvh * p.G + (valid ? (int)(r % p.G) : 0);
+      {  // the query rows: half of a row per thread
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)j * p.q_stride + (size_t)hq * D) + wg * (D / 16);
+        uint4 v[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) v[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = wg * (D / 16) + i;
+          *reinterpret_cast<uint4*>(smem + Ly::oQ + (c / 8) * (kRows * 128) + swz(row, c % 8)) = v[i];
+        }
+        fence_async_smem();
+        mbar_arrive(q_full);
+      }
+      int lo = 0, hi = 0;
+      if (valid) interval(p, j, lo, hi);
+      const int pos = p.H + j;
+      float slope = 0.f;
+      if constexpr (kSlope) slope = valid ? -__ldg(p.slopes + hq) * kLog2e : 0.f;
+      const int lo_in = rg[w.rb].lo_in, hi_in = rg[w.rb].hi_in;
+      // with a bias, tiles with keys behind the row's own position take the general path too
+      const int lin_end = kSlope ? min(hi_in, p.H + (int)((int64_t)w.rb * kRows / p.G) + 1) : hi_in;
+      float l = 0.f, Mown = -INFINITY;
+      for (int t = 0; t < w.len; ++t, ++n) {
+        if ((n & 1) != wg) continue;
+        const int key0 = (w.lo + w.first + t) * kKeys;
+        pwait(&sc_full[n % 8], (n / 8) & 1, abort_flag);
+        const float* sc = reinterpret_cast<const float*>(smem + Ly::oSc) + (n % 8) * kScales;
+        pwait(&s_full[n & 1], (n >> 1) & 1, abort_flag);
+        tc_fence_after();
+        const uint32_t ts = trow + (n & 1) * kKeys;
+        float v[kKeys];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+        tmem_wait_ld();
+        const bool inside = key0 >= lo_in && key0 + kKeys <= lin_end;  // the same in every thread
+        // u = score log2 e (+ bias) + log2 sV
+#pragma unroll
+        for (int b = 0; b < kBlk; ++b) {
+          const float ks = sc[b], lv = sc[kBlk + b];
+          float base = lv;
+          if constexpr (kSlope) base = __fmaf_rn(slope, (float)(pos - key0 - b * kBS), lv);  // minus slope x offset, below
+          const uint64_t ks2 = f2(ks, ks);
+#pragma unroll
+          for (int i = b * kBS; i < (b + 1) * kBS; i += 2) {
+            float add0 = base, add1 = base;
+            if constexpr (kSlope) {
+              add0 = __fmaf_rn(-slope, (float)(i - b * kBS), base);
+              add1 = __fmaf_rn(-slope, (float)(i + 1 - b * kBS), base);
+            }
+            if constexpr (kCap) {
+              float x0, x1;
+              f2_split(mul2(f2(v[i], v[i + 1]), ks2), x0, x1);
+              v[i] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(x0) + 1.f), p.cap_log2 + add0);
+              v[i + 1] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(x1) + 1.f), p.cap_log2 + add1);
+            } else {
+              f2_split(fma2(f2(v[i], v[i + 1]), ks2, f2(add0, add1)), v[i], v[i + 1]);
+            }
+          }
+        }
+        if (!inside) {
+          const int a = lo - key0, e = hi - key0;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) {
+            if constexpr (kSlope) {  // keys behind the row: |pos - t|, the linear form has the other sign
+              const int d = key0 + i - pos;
+              if (d > 0) v[i] = __fmaf_rn(2.f * slope, (float)d, v[i]);
+            }
+            if (i < a || i >= e) v[i] = -INFINITY;
+          }
+        }
+        float mx = max3(v[0], v[1], v[2]);
+#pragma unroll
+        for (int i = 3; i + 1 < kKeys; i += 2) mx = max3(mx, v[i], v[i + 1]);
+        mx = fmaxf(mx, v[kKeys - 1]);
+        // the running maximum: from the neighbour's tile, to the neighbour's next
+        float M = -INFINITY;
+        if (t > 0) {
+          pwait(&m_full[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag);
+          M = mref[((n - 1) & 1) * kRows + row];
+        }
+        float alpha = 1.f;
+        if (mx > M + kLazy || M == -INFINITY) {
+          if (M != -INFINITY) alpha = ex2(M - mx);
+          M = mx;
+        }
+        mref[(n & 1) * kRows + row] = M;
+        mbar_arrive(&m_full[n & 1]);
+        const float m0 = M == -INFINITY ? 0.f : M;  // a row that has seen no key yet
+        if (Mown != M) {
+          l = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
+          Mown = M;
+        }
+        uint32_t pk[32], pl[kHiLo ? 32 : 1];
+        const uint64_t nm = f2(-m0, -m0);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int b = 4 * half; b < 4 * half + 4; ++b) {
+            uint64_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < kBS; i += 2) {
+              float x0, x1;
+              f2_split(add2(f2(v[b * kBS + i], v[b * kBS + i + 1]), nm), x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              sum = i == 0 ? f2(x0, x1) : add2(sum, f2(x0, x1));
+              const int at = (b - 4 * half) * 8 + i / 2;
+              pk[at] = f16x2_of(x0, x1);
+              if constexpr (kHiLo) pl[at] = f16x2_rest(pk[at], x0, x1);
+            }
+            float s0, s1;
+            f2_split(sum, s0, s1);
+            const float inv = sc[2 * kBlk + b];
+            if (inv < 0.f && s0 + s1 > 0.f) record_error(2);  // a table entry outside the pool, and a row that sees it
+            l = __fmaf_rn(s0 + s1, fabsf(inv), l);
+          }
+          tmem_st32(ts + 32 * half, pk);
+          if constexpr (kHiLo) tmem_st32(ts + 64 + 32 * half, pl);
+        }
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // rare: O joins the new maximum
+          pwait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            uint32_t ob[32];
+            tmem_ld32(trow + Ly::kOCol + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ob[i] = __float_as_uint(o[i] * alpha);
+            tmem_st32(trow + Ly::kOCol + 32 * c, ob);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[n & 1]);
+      }
+      // ---- the end of the segment: O / l, or a record ----
+      const int last = n - 1;
+      named_bar_sync(1, 2 * kWG);  // both warpgroups are through their tiles: S(last) was complete
+      pwait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
+      tc_fence_after();
+      stat[(wg * 2 + 0) * kRows + row] = l;
+      stat[(wg * 2 + 1) * kRows + row] = Mown;
+      named_bar_sync(1, 2 * kWG);
+      const float M = mref[(last & 1) * kRows + row];
+      float lsum = 0.f;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float m = stat[(g * 2 + 1) * kRows + row];
+        if (m != -INFINITY) lsum = __fmaf_rn(stat[g * 2 * kRows + row], ex2(m - M), lsum);
+      }
+      const bool whole = w.first == 0 && w.len == w.cnt;
+      const float iv = lsum > 0.f ? 1.0f / lsum : 0.f;
+      const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
+      float* rec = reinterpret_cast<float*>(ws + pp.w.oRec) + (size_t)slot * kRows * (D + 2);
+      const size_t orow = ((size_t)j * p.Hq + hq) * D;
+#pragma unroll 1
+      for (int c = wg * (D / 64); c < (wg + 1) * (D / 64); ++c) {
+        float o[32];
+        tmem_ld32(trow + Ly::kOCol + 32 * c, o);
+        tmem_wait_ld();
+        if (whole) {
+          if (valid) {
+            if (p.out_bf16) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + 32 * c + i) =
+                    make_uint4(bf16x2_rn(o[i] * iv, o[i + 1] * iv), bf16x2_rn(o[i + 2] * iv, o[i + 3] * iv),
+                               bf16x2_rn(o[i + 4] * iv, o[i + 5] * iv), bf16x2_rn(o[i + 6] * iv, o[i + 7] * iv));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + 32 * c + i) =
+                    make_float4(o[i] * iv, o[i + 1] * iv, o[i + 2] * iv, o[i + 3] * iv);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(rec + (size_t)row * D + 32 * c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
+      }
+      if (!whole && wg == 0) {
+        rec[kRows * D + row] = M;
+        rec[kRows * D + kRows + row] = lsum;
+      }
+      tc_fence_before();
+      mbar_arrive(o_free);
+      named_bar_sync(1, 2 * kWG);  // the statistics are read: the query tile may be rewritten
+      first_seg = false;
+    } while (walk_next(pp, rg, w));
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Row blocks that span CTAs, merged in CTA order: a warp per row; the grid runs
+// over the places where the list is cut and the rows, and a row block's first cut
+// has its merge.
+template <int D>
+__global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_constant__ Params pp) {
+  const BlockDecodeParams& p = pp.a;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int cut = blockIdx.x / (kRows / 8) + 1, row = (blockIdx.x % (kRows / 8)) * 8 + (threadIdx.x >> 5);
+  uint8_t* ws = static_cast<uint8_t*>(p.ws);
+  const Head h = reinterpret_cast<const Head*>(ws + pp.w.oHead)[cut];
+  if (h.rb < 0 || h.first == 0) return;
+  const int64_t r = (int64_t)h.rb * kRows + row;
+  if (r >= (int64_t)p.C * p.G) return;
+  const int grid = pp.w.grid, total = h.total;
+  const int a = cut_at(total, grid, cut) - h.first, e = a + h.cnt;
+  const int c0 = cta_of(total, grid, a), c1 = cta_of(total, grid, e - 1);
+  if (cut != c0 + 1) return;
+  constexpr int E = D / 32;
+  float acc[E], M = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    // a CTA whose range starts inside the row block has it as its first segment
+    const int slot = 2 * c + (cut_at(total, grid, c) >= a ? 0 : 1);
+    const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)slot * kRows * (D + 2);
+    float x[E];
+    const float* src = rec + (size_t)row * D + lane * E;
+    if constexpr (E == 2) {
+      const float2 t = *reinterpret_cast<const float2*>(src);
+      x[0] = t.x;
+      x[1] = t.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(src + i);
+        x[i] = t.x;
+        x[i + 1] = t.y;
+        x[i + 2] = t.z;
+        x[i + 3] = t.w;
+      }
+    }
+    const float m = rec[kRows * D + row], ll = rec[kRows * D + kRows + row];
+    const float nm = fmaxf(M, m);
+    if (nm != -INFINITY) {
+      const float f = ex2(M - nm), k = ex2(m - nm);
+#pragma unroll
+      for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + x[i] * k;
+      l = l * f + ll * k;
+      M = nm;
+    }
+  }
+  const float iv = l > 0.f ? 1.0f / l : 0.f;
+  const size_t o = ((size_t)(r / p.G) * p.Hq + h.kvh * p.G + r % p.G) * D + lane * E;
+#pragma unroll
+  for (int i = 0; i < E; i += 2) {
+    if (p.out_bf16)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + i) = bf16x2_rn(acc[i] * iv, acc[i + 1] * iv);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + i) = make_float2(acc[i] * iv, acc[i + 1] * iv);
+  }
+}
+
+template <int D, bool kCap, bool kSlope, bool kHiLo>
+cudaError_t launch(const Params& pp, cudaStream_t stream) {
+  auto* kernel = block_prefix_kernel<D, kCap, kSlope, kHiLo>;
+  // the shared-memory opt-in, once per device (graph captures then make no attribute call)
+  int dev = 0;
+  cudaGetDevice(&dev);
+  static bool opted[64] = {false};
+  if (dev < 0 || dev >= 64 || !opted[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kTotal);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) opted[dev] = true;
+  }
+  cudaError_t e = launch_pdl(block_tiles_kernel<D>, dim3(pp.w.ntiles, pp.a.Hkv), dim3(256), 0, stream, pp);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(pp.w.grid), dim3(kThreads), Lay<D>::kTotal, stream, pp);
+  if (e != cudaSuccess || pp.w.grid == 1) return e;
+  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * (kRows / 8)), dim3(256), 0, stream, pp);
+}
+
+template <int D, bool kHiLo>
+cudaError_t launch_w(const Params& pp, cudaStream_t stream) {
+  const bool cap = pp.a.cap_log2 > 0.f, slope = pp.a.slopes != nullptr;
+  if (cap) return slope ? launch<D, true, true, kHiLo>(pp, stream) : launch<D, true, false, kHiLo>(pp, stream);
+  return slope ? launch<D, false, true, kHiLo>(pp, stream) : launch<D, false, false, kHiLo>(pp, stream);
+}
+
+template <int D>
+cudaError_t launch_any(const Params& pp, cudaStream_t stream) {
+  return pp.a.out_bf16 ? launch_w<D, false>(pp, stream) : launch_w<D, true>(pp, stream);
+}
+
+}  // namespace bp
+}  // namespace i8kv

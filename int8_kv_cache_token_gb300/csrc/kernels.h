@@ -166,6 +166,9 @@ cudaError_t read_error_decode(int* value);
 cudaError_t read_error_prefix(int* value);
 cudaError_t read_error_block_cache(int* value);
 cudaError_t read_error_block_decode(int* value);
+cudaError_t read_error_block_prefix_64(int* value);
+cudaError_t read_error_block_prefix_128(int* value);
+cudaError_t read_error_block_prefix_256(int* value);
 
 cudaError_t launch_kv_quant_write(const ProducerParams& p, cudaStream_t stream);
 cudaError_t launch_kv_rope_quant_write(const ProducerParams& p, cudaStream_t stream);
@@ -193,6 +196,10 @@ cudaError_t launch_block_kv_read(const BlockRaggedParams& r, const BlockReadPara
 int block_decode_grid(int entries, int HH, int max_blocks);
 size_t block_decode_workspace_bytes(int D, int grid);
 cudaError_t launch_block_decode(const BlockDecodeParams& p, cudaStream_t stream);
+// A chunk: few rows run in groups of eight (block_decode.cu), more in 128-row
+// blocks on the tensor cores (block_prefix.cuh).  p.grid and p.ws are set here.
+size_t block_prefix_workspace_bytes(int H, int C, int G, int Hkv, int D);
+cudaError_t launch_block_prefix(BlockDecodeParams p, cudaStream_t stream);
 cudaError_t launch_block_chunk_rows(const BlockDecodeParams& p, cudaStream_t stream);
 
 }  // namespace i8kv

@@ -310,6 +310,49 @@ def test_chunk_variants(D, kw):
     _chunk(D, 4, 4, 0, 130, seed=D + 1, **kw)
 
 
+@pytest.mark.parametrize("D, Hq, Hkv, H, C", [(64, 16, 2, 2900, 701), (128, 8, 4, 40, 2100), (256, 24, 4, 1000, 1300), (128, 32, 8, 9000, 33)])
+@pytest.mark.parametrize("kw", [dict(), dict(cap=40.0, begin=docs), dict(window=300, slopes=True), dict(begin=holes, dtype=torch.float32),
+                                dict(end=prefix, slopes=True, dtype=torch.float32, cap=15.0)])
+def test_chunk_long(D, Hq, Hkv, H, C, kw):
+    """Many row blocks and tiles: row blocks cut over CTAs, CTAs with several row blocks."""
+    _chunk(D, Hq, Hkv, H, C, seed=D + C, sample=10, **kw)
+
+
+def test_chunk_hidden_blocks_and_bad_tables():
+    """Blocks that no row sees may have any table entry and any scale; an entry outside the pool that a row sees is recorded."""
+    rng = np.random.default_rng(30)
+    H, C, Hq, Hkv, D = 400, 100, 8, 2, 128
+    table, nb = tables(rng, [H + C])
+    c = Cache(nb, Hkv, D).random(rng)
+    q = dev_bf16(rng.standard_normal((C, Hq, D)))
+    outs = []
+    begin = dev(np.full(C, 200, np.int32))
+    for spoil in (False, True):
+        t = table[0].copy()
+        if spoil:
+            for w in "kv":
+                c.scale[w][t[:12]] = np.nan
+                c.scale[w][[i for i in range(nb) if i not in set(t)]] = np.inf
+            t[:6] = -1
+            t[6:9] = nb + 100
+        out = torch.empty((C, Hq, D), dtype=torch.float32, device="cuda")
+        i8.block_prefix_attn(out, q, **upload(c), block_table=dev(t), history_len=H, key_begin=begin)
+        outs.append(out)
+        assert i8.device_error() == 0
+    assert torch.equal(outs[0], outs[1])
+    for C2 in (100, 3):
+        t = table[0].copy()
+        t[20] = nb
+        i8.block_prefix_attn(outs[0][:C2], q[:C2], **upload(c), block_table=dev(t), history_len=H, key_begin=begin[:C2])
+        assert i8.device_error() == 2
+
+
+def test_chunk_rows_at_the_limits_of_both_routes():
+    """Numbers of (token, head) rows around the change of route and around a row block."""
+    for C in (63, 64, 65, 127, 128, 129):
+        _chunk(64, 2, 2, 77, C, torch.float32, seed=C)
+
+
 # ------------------------------------------------------------------------------------------------- together
 def test_prefill_then_decode():
     """As a server uses them: two sequences prefilled in chunks, then decoded token by token; the decode of the newest
