@@ -442,12 +442,27 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
       float u[4] = {s[0][0] + s[1][0], s[0][1] + s[1][1], s[0][2] + s[1][2], s[0][3] + s[1][3]};
       const int key0 = (w.s.fb + w.first + i) * kBS;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = u[j] * ((j & 1) ? c1 : c0);
-        if constexpr (kCap)
-          u[j] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(x) + 1.f), p.cap_log2 + lv);
-        else
-          u[j] = x + lv;
+      for (int j = 0; j < 4; ++j) u[j] *= (j & 1) ? c1 : c0;
+      if constexpr (kCap) {
+        // u = score / cap here; cap log2 e tanh u, by the polynomial in u^2 for |u| <= 1
+        if (__any_sync(0xffffffffu, !(fmaxf(fmaxf(fabsf(u[0]), fabsf(u[1])), fmaxf(fabsf(u[2]), fabsf(u[3]))) <= 1.f))) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            u[j] = kHiLo ? __fmaf_rn(p.cap_log2, tanhf(u[j]), lv)
+                         : __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(u[j] * (2.f * kLog2e)) + 1.f), p.cap_log2 + lv);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float y = u[j] * u[j];
+            float a = p.cap_poly[kCapDeg];
+#pragma unroll
+            for (int d = kCapDeg - 1; d >= 0; --d) a = __fmaf_rn(a, y, p.cap_poly[d]);
+            u[j] = __fmaf_rn(a, u[j], lv);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[j] += lv;
       }
       if (p.slopes != nullptr) {
         u[0] = __fmaf_rn(sl0, (float)abs(key0 + tok0 - pos0), u[0]);

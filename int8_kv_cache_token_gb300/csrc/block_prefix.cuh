@@ -28,8 +28,8 @@
 // third kernel.  So a causal triangle, a window, packed documents and a short
 // chunk over a long history all fill the GPU.
 //
-// Warps: 0 tile copies (one lane), 1 MMA issue (one lane), 2 tensor memory, 4-7
-// and 8-11 softmax.  One thread issues both products: MMAs of a CTA execute in
+// Warps: 0 tile copies, 1 MMA issue, 2 tensor memory, 4-7 and 8-11 softmax.  One
+// thread issues both products: MMAs of a CTA execute in
 // issue order, which is what lets W share its S slot with the S after next.
 #pragma once
 
@@ -95,12 +95,13 @@ struct Lay {
   static constexpr int kParts = D == 64 ? 1 : 2;       // stages per operand tile
   static constexpr int kTile = kKeys * D * 2;
   static constexpr int kStage = kTile / kParts;        // K: half the dims; V: half the keys
-  static constexpr int kStages = D == 256 ? 5 : 12;
+  static constexpr int kStages = D == 256 ? 5 : D == 128 ? 11 : 12;
   static constexpr int kQ = kRows * D * 2;
-  static constexpr int oQ = 0;                         // [D/64][128 rows][128 B], then the row statistics
+  static constexpr int oQ = 0;                         // [D/64][128 rows][128 B]
   static constexpr int oRing = oQ + kQ;
   static constexpr int oM = oRing + kStages * kStage;  // M [2][128]
-  static constexpr int oSc = oM + 2 * kRows * 4;       // scales of 8 tiles
+  static constexpr int oL = oM + 2 * kRows * 4;        // the warpgroups' row sums [2][128]
+  static constexpr int oSc = oL + 2 * kRows * 4;       // scales of 8 tiles
   static constexpr int oBar = oSc + 8 * kScales * 4;
   // full[kStages], free[kStages], sc_full[8], s_full[2], p_full[2], m_full[2], pv_done[2], q_full, o_free
   static constexpr int kBars = 2 * kStages + 8 + 2 + 2 + 2 + 2 + 2;
@@ -236,13 +237,16 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
   }
 }
 
+// A value that is the same in every lane, known as such to the compiler.
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ---- the walk over a CTA's range of the list (KV head, row block, tile)
 struct Walk {
   int kvh, rb, first, len, left, cnt, lo;  // segment: tiles lo + first .. + len of the row block
 };
 __device__ __forceinline__ void walk_load(const Range* rg, Walk& w) {
-  w.lo = rg[w.rb].lo;
-  w.cnt = rg[w.rb].hi - w.lo;
+  w.lo = uni(rg[w.rb].lo);
+  w.cnt = uni(rg[w.rb].hi) - w.lo;
   w.len = min(w.cnt - w.first, w.left);
 }
 __device__ __forceinline__ bool walk_next(const Params& pp, const Range* rg, Walk& w) {
@@ -278,6 +282,41 @@ __device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, volatile i
       record_error(1);
       *abort_flag = 1;
       return;
+    }
+  }
+}
+// The same for a whole warp that stays together; false once the CTA has aborted.
+__device__ __forceinline__ bool pwait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  pwait(bar, parity, abort_flag);
+  return !__any_sync(0xffffffffu, *abort_flag != 0);
+}
+// One lane of a converged warp.  The copies and MMAs are issued under it by a
+// warp whose control flow is uniform, so their operands live in uniform
+// registers: issued by "lane 0" of a divergent branch each MMA took about 150
+// cycles to hand over, longer than it runs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// 16-byte units of 32 rows: lane i of a group of U lanes holds units 0 .. U - 1 of
+// row i of the group; afterwards unit i of its rows 0 .. U - 1.
+template <int U>
+__device__ __forceinline__ void transpose_units(uint4 (&u)[U], int lane) {
+#pragma unroll
+  for (int s = 1; s < U; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (k & s) continue;
+      uint4 send = up ? u[k] : u[k | s], got;
+      got.x = __shfl_xor_sync(0xffffffffu, send.x, s);
+      got.y = __shfl_xor_sync(0xffffffffu, send.y, s);
+      got.z = __shfl_xor_sync(0xffffffffu, send.z, s);
+      got.w = __shfl_xor_sync(0xffffffffu, send.w, s);
+      if (up) u[k] = got;
+      else u[k | s] = got;
     }
   }
 }
@@ -317,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   uint64_t* o_free = q_full + 1;    // the segment's O is read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::oCtl);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::oCtl + 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const Range* rg = reinterpret_cast<const Range*>(ws + pp.w.oRange);
 
@@ -342,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = (uint32_t)uni((int)*tmem_slot);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -374,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
     per_head += scan_step(rb < pp.w.nrb ? rg[rb].hi - rg[rb].lo : 0, before);
   }
   const int total = per_head * p.Hkv;
-  const int u0 = cut_at(total, grid, blockIdx.x), u1 = cut_at(total, grid, blockIdx.x + 1);
+  const int u0 = uni(cut_at(total, grid, blockIdx.x)), u1 = uni(cut_at(total, grid, blockIdx.x + 1));
   if (tid < 2) scan[16 + tid] = 0;
   const int kvh0 = per_head > 0 ? u0 / per_head : 0;
   {
@@ -394,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   __syncthreads();
   Walk w;
   w.kvh = kvh0;
-  w.rb = scan[16];
-  w.first = scan[17];
+  w.rb = uni(scan[16]);
+  w.first = uni(scan[17]);
   w.left = u1 - u0;
   walk_load(rg, w);
   if (tid == 0) {
@@ -422,97 +461,125 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
 
   if (warp < kSoftWarp) {
     regs_dec<kRegsCtl>();
-    if (u0 < u1 && warp == 0 && lane == 0) {
+    if (u0 < u1 && warp == 0) {
       // ================= tile copies =================
-      int c = 0, n = 0;  // stages filled, tiles of K
+      int st = 0, lap = 0, c = 0, n = 0;  // next stage, laps of the ring; stages filled, tiles of K
       const uint8_t* src[2] = {ws + pp.w.oK, ws + pp.w.oV};
       const float* scl = reinterpret_cast<const float*>(ws + pp.w.oScale);
+      bool ok = true;
       auto load = [&](int which, size_t ti) {
 #pragma unroll
-        for (int h = 0; h < Ly::kParts; ++h, ++c) {
-          const int st = c % NS;
-          if (c >= NS) pwait(&free_[st], ((c / NS) - 1) & 1, abort_flag);
-          if (*abort_flag) return;
-          mbar_expect_tx(&full[st], Ly::kStage);
-          bulk_g2s(smem + Ly::oRing + st * Ly::kStage, src[which] + ti * Ly::kTile + h * Ly::kStage, Ly::kStage, &full[st]);
-          mbar_arrive(&full[st]);
+        for (int h = 0; h < Ly::kParts; ++h) {
+          if (ok && lap > 0) ok = pwait_warp(&free_[st], (lap - 1) & 1, abort_flag);
+          if (!ok) return;
+          if (elect_one()) {
+            mbar_expect_tx(&full[st], Ly::kStage);
+            bulk_g2s(smem + Ly::oRing + st * Ly::kStage, src[which] + ti * Ly::kTile + h * Ly::kStage, Ly::kStage, &full[st]);
+            mbar_arrive(&full[st]);
+            if (which == 0 && h == 0) {
+              uint64_t* b = &sc_full[n % 8];
+              mbar_expect_tx(b, kScales * 4);
+              bulk_g2s(smem + Ly::oSc + (n % 8) * kScales * 4, scl + ti * kScales, kScales * 4, b);
+              mbar_arrive(b);
+            }
+          }
+          __syncwarp();
+          ++c;
+          if (++st == NS) {
+            st = 0;
+            ++lap;
+          }
         }
-        if (which == 0) {
-          uint64_t* b = &sc_full[n % 8];
-          mbar_expect_tx(b, kScales * 4);
-          bulk_g2s(smem + Ly::oSc + (n % 8) * kScales * 4, scl + ti * kScales, kScales * 4, b);
-          mbar_arrive(b);
-          ++n;
-        }
+        n += which == 0;
       };
       do {
         const size_t t0 = (size_t)w.kvh * pp.w.ntiles + (w.lo + w.first - pp.w.tile0);
         load(0, t0);
-        for (int t = 0; t < w.len && !*abort_flag; ++t) {
+        for (int t = 0; t < w.len && ok; ++t) {
           if (t + 1 < w.len) load(0, t0 + t + 1);
           load(1, t0 + t);
         }
-      } while (!*abort_flag && walk_next(pp, rg, w));
-      if (*abort_flag) {  // copies under way land before the CTA exits
+      } while (ok && walk_next(pp, rg, w));
+      if (!ok) {  // copies under way land before the CTA exits
         for (int k = max(0, c - NS); k < c; ++k) mbar_wait(&full[k % NS], (k / NS) & 1);
-        for (int k = max(0, n - 8); k < n; ++k) mbar_wait(&sc_full[k % 8], (k / 8) & 1);
+        for (int k = max(0, n - 7); k <= n; ++k) mbar_wait(&sc_full[k % 8], (k / 8) & 1);
       }
-    } else if (u0 < u1 && warp == 1 && lane == 0) {
+    } else if (u0 < u1 && warp == 1) {
       // ================= MMA issue =================
       constexpr uint32_t idesc_qk = umma_idesc_bf16(kRows, kKeys);
       constexpr uint32_t idesc_pv = umma_idesc_f16(kRows, D);
-      const uint32_t q0 = smem_u32(smem + Ly::oQ), ring = smem_u32(smem + Ly::oRing);
-      int c = 0, n = 0, seg = 0;
+      const uint64_t qdesc = umma_desc(smem_u32(smem + Ly::oQ), 128), rdesc = umma_desc(smem_u32(smem + Ly::oRing), 128);
+      int st = 0, lap = 0, n = 0, seg = 0;
       uint64_t* last = nullptr;
       uint32_t last_par = 0;
+      bool ok = true;
+      auto next_stage = [&]() {
+        if (++st == NS) {
+          st = 0;
+          ++lap;
+        }
+      };
+      // a K = 16 step is 32 bytes of a 128-byte row; the descriptors count 16-byte units
       auto qk = [&](int m) {  // S of the CTA's tile m
 #pragma unroll
-        for (int h = 0; h < Ly::kParts; ++h, ++c) {
-          const int st = c % NS;
-          pwait(&full[st], (c / NS) & 1, abort_flag);
+        for (int h = 0; h < Ly::kParts; ++h) {
+          if (ok) ok = pwait_warp(&full[st], lap & 1, abort_flag);
+          if (!ok) return;
           tc_fence_after();
           constexpr int kSteps = D / 16 / Ly::kParts;
+          const uint64_t kd = rdesc + (uint64_t)(st * (Ly::kStage / 16));
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            const int kk = h * kSteps + k;
-            umma_f16(tmem + (m & 1) * kKeys, umma_desc(q0 + (kk / 4) * (kRows * 128) + (kk % 4) * 32, 128),
-                     umma_desc(ring + st * Ly::kStage + (k / 4) * (kKeys * 128) + (k % 4) * 32, 128), idesc_qk, kk > 0);
+            for (int k = 0; k < kSteps; ++k) {
+              const int kk = h * kSteps + k;
+              umma_f16(tmem + (m & 1) * kKeys, qdesc + (kk / 4) * (kRows * 8) + (kk % 4) * 2,
+                       kd + (k / 4) * (kKeys * 8) + (k % 4) * 2, idesc_qk, kk > 0);
+            }
+            umma_commit(&free_[st]);
+            if (h == Ly::kParts - 1) umma_commit(&s_full[m & 1]);
           }
-          umma_commit(&free_[st]);
+          __syncwarp();
+          next_stage();
         }
-        umma_commit(&s_full[m & 1]);
         last = &s_full[m & 1];
         last_par = (m >> 1) & 1;
       };
       do {
-        pwait(q_full, seg & 1, abort_flag);
+        ok = pwait_warp(q_full, seg & 1, abort_flag);
         qk(n);
-        for (int t = 0; t < w.len && !*abort_flag; ++t, ++n) {
+        for (int t = 0; t < w.len && ok; ++t, ++n) {
           if (t + 1 < w.len) qk(n + 1);
-          pwait(&p_full[n & 1], (n >> 1) & 1, abort_flag);
-          if (t == 0 && seg > 0) pwait(o_free, (seg - 1) & 1, abort_flag);
-          if (*abort_flag) break;
+          if (ok) ok = pwait_warp(&p_full[n & 1], (n >> 1) & 1, abort_flag);
+          if (ok && t == 0 && seg > 0) ok = pwait_warp(o_free, (seg - 1) & 1, abort_flag);
 #pragma unroll
-          for (int h = 0; h < Ly::kParts; ++h, ++c) {
-            const int st = c % NS;
-            pwait(&full[st], (c / NS) & 1, abort_flag);
+          for (int h = 0; h < Ly::kParts; ++h) {
+            if (ok) ok = pwait_warp(&full[st], lap & 1, abort_flag);
+            if (!ok) break;
             tc_fence_after();
             constexpr int kSteps = kKeys / 16 / Ly::kParts;
+            const uint64_t vd = rdesc + (uint64_t)(st * (Ly::kStage / 16));
+            const uint32_t wt = tmem + (n & 1) * kKeys;
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              const int kk = h * kSteps + k;
-              const uint64_t vd = umma_desc(ring + st * Ly::kStage + (k / 4) * (D * 128) + (k % 4) * 32, 128);
-              umma_f16_ta(tmem + Ly::kOCol, tmem + (n & 1) * kKeys + kk * 8, vd, idesc_pv, t > 0 || kk > 0);
-              if constexpr (kHiLo) umma_f16_ta(tmem + Ly::kOCol, tmem + (n & 1) * kKeys + 64 + kk * 8, vd, idesc_pv, true);
+              for (int k = 0; k < kSteps; ++k) {
+                const int kk = h * kSteps + k;
+                const uint64_t b = vd + (k / 4) * (D * 8) + (k % 4) * 2;
+                umma_f16_ta(tmem + Ly::kOCol, wt + kk * 8, b, idesc_pv, t > 0 || kk > 0);
+                if constexpr (kHiLo) umma_f16_ta(tmem + Ly::kOCol, wt + 64 + kk * 8, b, idesc_pv, true);
+              }
+              umma_commit(&free_[st]);
+              if (h == Ly::kParts - 1) umma_commit(&pv_done[n & 1]);
             }
-            umma_commit(&free_[st]);
+            __syncwarp();
+            next_stage();
           }
-          umma_commit(&pv_done[n & 1]);
-          last = &pv_done[n & 1];
-          last_par = (n >> 1) & 1;
+          if (ok) {
+            last = &pv_done[n & 1];
+            last_par = (n >> 1) & 1;
+          }
         }
         ++seg;
-      } while (!*abort_flag && walk_next(pp, rg, w));
+      } while (ok && walk_next(pp, rg, w));
       if (last) mbar_wait(last, last_par);  // every MMA has completed before tensor memory is released
     }
     __syncwarp();
@@ -523,35 +590,54 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
     const int row = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     float* mref = reinterpret_cast<float*>(smem + Ly::oM);
-    float* stat = reinterpret_cast<float*>(smem + Ly::oQ);  // [wg][l, M][128], once the query tile is read
-    const int64_t R = (int64_t)p.C * p.G;
-    int n = 0;
-    bool first_seg = true;
-    if (u0 < u1) do {
-      const int64_t r = (int64_t)w.rb * kRows + row;
-      const bool valid = r < R;
-      const int j = valid ? (int)(r / p.G) : 0, hq = w.kvh * p.G + (valid ? (int)(r % p.G) : 0);
-      {  // the query rows: half of a row per thread
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)j * p.q_stride + (size_t)hq * D) + wg * (D / 16);
-        uint4 v[D / 16];
+    float* lrow = reinterpret_cast<float*>(smem + Ly::oL);
+    const int R = p.C * p.G;
+    // The query rows of a segment: 16 rows per warp, whole rows by neighbouring
+    // lanes, held in registers until the previous segment's products have read
+    // the tile in shared memory.
+    constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes per row, rows per load
+    constexpr int kLoads = 16 / kAt;
+    uint4 qv[kLoads];
+    const int qrow0 = (warp - kSoftWarp) * 16 + lane / kLanes;
+    auto load_q = [&](const Walk& x) {
+      const int r = x.rb * kRows + qrow0;
+      int j = r / p.G, h = r % p.G;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) v[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int c = wg * (D / 16) + i;
-          *reinterpret_cast<uint4*>(smem + Ly::oQ + (c / 8) * (kRows * 128) + swz(row, c % 8)) = v[i];
+      for (int i = 0; i < kLoads; ++i) {
+        qv[i] = make_uint4(0, 0, 0, 0);
+        if (r + i * kAt < R)
+          qv[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)j * p.q_stride + (size_t)(x.kvh * p.G + h) * D) +
+                        lane % kLanes);
+        h += kAt;
+        while (h >= p.G) {
+          h -= p.G;
+          ++j;
         }
-        fence_async_smem();
-        mbar_arrive(q_full);
       }
+    };
+    auto store_q = [&]() {
+      const int c = lane % kLanes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        *reinterpret_cast<uint4*>(smem + Ly::oQ + (c / 8) * (kRows * 128) + swz(qrow0 + i * kAt, c % 8)) = qv[i];
+      fence_async_smem();
+      mbar_arrive(q_full);
+    };
+    int n = 0;
+    bool first_seg = true, more = u0 < u1;
+    if (more) {
+      load_q(w);
+      store_q();
+    }
+    while (more) {
+      const int r = w.rb * kRows + row;
+      const bool valid = r < R;
+      const int j = valid ? r / p.G : 0, hq = w.kvh * p.G + (valid ? r % p.G : 0);
       int lo = 0, hi = 0;
       if (valid) interval(p, j, lo, hi);
       const int pos = p.H + j;
       float slope = 0.f;
       if constexpr (kSlope) slope = valid ? -__ldg(p.slopes + hq) * kLog2e : 0.f;
-      const int lo_in = rg[w.rb].lo_in, hi_in = rg[w.rb].hi_in;
-      // with a bias, tiles with keys behind the row's own position take the general path too
-      const int lin_end = kSlope ? min(hi_in, p.H + (int)((int64_t)w.rb * kRows / p.G) + 1) : hi_in;
       float l = 0.f, Mown = -INFINITY;
       for (int t = 0; t < w.len; ++t, ++n) {
         if ((n & 1) != wg) continue;
@@ -559,52 +645,87 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         pwait(&sc_full[n % 8], (n / 8) & 1, abort_flag);
         const float* sc = reinterpret_cast<const float*>(smem + Ly::oSc) + (n % 8) * kScales;
         pwait(&s_full[n & 1], (n >> 1) & 1, abort_flag);
+        __syncwarp();
         tc_fence_after();
         const uint32_t ts = trow + (n & 1) * kKeys;
         float v[kKeys];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
         tmem_wait_ld();
-        const bool inside = key0 >= lo_in && key0 + kKeys <= lin_end;  // the same in every thread
+        // the block's addend of offset i: log2 sV, and with a bias slope (pos - key)
+        auto addend = [&](int b, int i) {
+          float base = sc[kBlk + b];
+          if constexpr (kSlope)
+            base = __fmaf_rn(-slope, (float)i, __fmaf_rn(slope, (float)(pos - key0 - b * kBS), base));
+          return base;
+        };
         // u = score log2 e (+ bias) + log2 sV
+        if constexpr (kCap) {
+          // z = score / cap; cap log2 e tanh z = z P(z^2) for |z| <= 1: P interpolates
+          // tanh(z) / z at Chebyshev nodes (5e-8 relative), on the FMA pipes that the
+          // exponentials leave idle
+          float ymax = 0.f;
 #pragma unroll
-        for (int b = 0; b < kBlk; ++b) {
-          const float ks = sc[b], lv = sc[kBlk + b];
-          float base = lv;
-          if constexpr (kSlope) base = __fmaf_rn(slope, (float)(pos - key0 - b * kBS), lv);  // minus slope x offset, below
-          const uint64_t ks2 = f2(ks, ks);
+          for (int b = 0; b < kBlk; ++b) {
+            const uint64_t ks2 = f2(sc[b], sc[b]);
 #pragma unroll
-          for (int i = b * kBS; i < (b + 1) * kBS; i += 2) {
-            float add0 = base, add1 = base;
-            if constexpr (kSlope) {
-              add0 = __fmaf_rn(-slope, (float)(i - b * kBS), base);
-              add1 = __fmaf_rn(-slope, (float)(i + 1 - b * kBS), base);
-            }
-            if constexpr (kCap) {
-              float x0, x1;
-              f2_split(mul2(f2(v[i], v[i + 1]), ks2), x0, x1);
-              v[i] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(x0) + 1.f), p.cap_log2 + add0);
-              v[i + 1] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(x1) + 1.f), p.cap_log2 + add1);
-            } else {
-              f2_split(fma2(f2(v[i], v[i + 1]), ks2, f2(add0, add1)), v[i], v[i + 1]);
+            for (int i = b * kBS; i < (b + 1) * kBS; i += 2) {
+              const uint64_t z = mul2(f2(v[i], v[i + 1]), ks2), y = mul2(z, z);
+              float y0, y1;
+              f2_split(y, y0, y1);
+              ymax = max3(ymax, y0, y1);
+              uint64_t a = f2(p.cap_poly[kCapDeg], p.cap_poly[kCapDeg]);
+#pragma unroll
+              for (int d = kCapDeg - 1; d >= 0; --d) a = fma2(a, y, f2(p.cap_poly[d], p.cap_poly[d]));
+              f2_split(fma2(a, z, f2(addend(b, i - b * kBS), addend(b, i + 1 - b * kBS))), v[i], v[i + 1]);
             }
           }
-        }
-        if (!inside) {
-          const int a = lo - key0, e = hi - key0;
+          if (__any_sync(0xffffffffu, !(ymax <= 1.f))) {  // some score above the cap: 1 - 2 / (e^2z + 1)
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) {
-            if constexpr (kSlope) {  // keys behind the row: |pos - t|, the linear form has the other sign
-              const int d = key0 + i - pos;
-              if (d > 0) v[i] = __fmaf_rn(2.f * slope, (float)d, v[i]);
+            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+            tmem_wait_ld();
+#pragma unroll
+            for (int b = 0; b < kBlk; ++b) {
+              const float ks = sc[b] * (2.f * kLog2e);
+#pragma unroll
+              for (int i = b * kBS; i < (b + 1) * kBS; ++i)
+                v[i] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(v[i] * ks) + 1.f), p.cap_log2 + addend(b, i - b * kBS));
             }
-            if (i < a || i >= e) v[i] = -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < kBlk; ++b) {
+            const uint64_t ks2 = f2(sc[b], sc[b]);
+#pragma unroll
+            for (int i = b * kBS; i < (b + 1) * kBS; i += 2)
+              f2_split(fma2(f2(v[i], v[i + 1]), ks2, f2(addend(b, i - b * kBS), addend(b, i + 1 - b * kBS))), v[i], v[i + 1]);
           }
         }
-        float mx = max3(v[0], v[1], v[2]);
+        if constexpr (kSlope) {  // keys behind the row: |pos - t|, the linear form has the other sign
+          if (__any_sync(0xffffffffu, key0 + kKeys - 1 > pos && hi > pos + 1)) {
+            const float d0 = (float)(key0 - pos);
 #pragma unroll
-        for (int i = 3; i + 1 < kKeys; i += 2) mx = max3(mx, v[i], v[i + 1]);
-        mx = fmaxf(mx, v[kKeys - 1]);
+            for (int i = 0; i < kKeys; ++i) v[i] = __fmaf_rn(2.f * slope, fmaxf(d0 + (float)i, 0.f), v[i]);
+          }
+        }
+        if (!__all_sync(0xffffffffu, key0 >= lo && key0 + kKeys <= hi)) {  // hidden keys: 32 at a time as bits
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int a = max(0, min(32, lo - key0 - 32 * c)), e = max(0, min(32, hi - key0 - 32 * c));
+            const uint32_t seen = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & ~(a == 32 ? 0xffffffffu : (1u << a) - 1u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[32 * c + i] = (seen >> i) & 1u ? v[32 * c + i] : -INFINITY;
+          }
+        }
+        float mb[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          mb[b] = max3(v[b * 16], v[b * 16 + 1], v[b * 16 + 2]);
+#pragma unroll
+          for (int i = 3; i + 1 < 16; i += 2) mb[b] = max3(mb[b], v[b * 16 + i], v[b * 16 + i + 1]);
+          mb[b] = fmaxf(mb[b], v[b * 16 + 15]);
+        }
+        const float mx = fmaxf(max3(max3(mb[0], mb[1], mb[2]), mb[3], mb[4]), max3(mb[5], mb[6], mb[7]));
         // the running maximum: from the neighbour's tile, to the neighbour's next
         float M = -INFINITY;
         if (t > 0) {
@@ -623,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
           l = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
           Mown = M;
         }
+        __syncwarp();
         uint32_t pk[32], pl[kHiLo ? 32 : 1];
         const uint64_t nm = f2(-m0, -m0);
 #pragma unroll
@@ -647,11 +769,13 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
             if (inv < 0.f && s0 + s1 > 0.f) record_error(2);  // a table entry outside the pool, and a row that sees it
             l = __fmaf_rn(s0 + s1, fabsf(inv), l);
           }
+          __syncwarp();
           tmem_st32(ts + 32 * half, pk);
           if constexpr (kHiLo) tmem_st32(ts + 64 + 32 * half, pl);
         }
         if (__any_sync(0xffffffffu, alpha != 1.f)) {  // rare: O joins the new maximum
           pwait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag);
+          __syncwarp();
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -668,61 +792,88 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         tc_fence_before();
         mbar_arrive(&p_full[n & 1]);
       }
-      // ---- the end of the segment: O / l, or a record ----
+      // ---- the end of the segment: O / l, or a record.  The next segment's query
+      // rows are on their way meanwhile, and its first product may start before O is read.
       const int last = n - 1;
+      Walk next = w;
+      more = walk_next(pp, rg, next);
+      if (more) load_q(next);
       named_bar_sync(1, 2 * kWG);  // both warpgroups are through their tiles: S(last) was complete
-      pwait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
-      tc_fence_after();
-      stat[(wg * 2 + 0) * kRows + row] = l;
-      stat[(wg * 2 + 1) * kRows + row] = Mown;
-      named_bar_sync(1, 2 * kWG);
       const float M = mref[(last & 1) * kRows + row];
-      float lsum = 0.f;
+      lrow[wg * kRows + row] = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
+      if (more) store_q();
+      named_bar_sync(1, 2 * kWG);
+      const float lsum = lrow[row] + lrow[kRows + row];
+      pwait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
+      __syncwarp();
+      tc_fence_after();
+      constexpr int kHalf = D / 2;  // columns per warpgroup
+      const uint32_t to = trow + Ly::kOCol + wg * kHalf;
+      if (w.first == 0 && w.len == w.cnt) {
+        const float iv = lsum > 0.f ? 1.0f / lsum : 0.f;
+        // 16-byte units, brought to whole 128-byte lines of a row by transposing
+        // among eight lanes (four for 64 bytes): a row per lane costs 32 lines a store
+        auto put = [&](auto& u, int col) {  // U units from column `col` of this warpgroup's half
+          constexpr int U = sizeof(u) / 16;
+          transpose_units<U>(u, lane);
+          const int unit = lane % U;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float m = stat[(g * 2 + 1) * kRows + row];
-        if (m != -INFINITY) lsum = __fmaf_rn(stat[g * 2 * kRows + row], ex2(m - M), lsum);
-      }
-      const bool whole = w.first == 0 && w.len == w.cnt;
-      const float iv = lsum > 0.f ? 1.0f / lsum : 0.f;
-      const int slot = 2 * blockIdx.x + (first_seg ? 0 : 1);
-      float* rec = reinterpret_cast<float*>(ws + pp.w.oRec) + (size_t)slot * kRows * (D + 2);
-      const size_t orow = ((size_t)j * p.Hq + hq) * D;
-#pragma unroll 1
-      for (int c = wg * (D / 64); c < (wg + 1) * (D / 64); ++c) {
-        float o[32];
-        tmem_ld32(trow + Ly::kOCol + 32 * c, o);
-        tmem_wait_ld();
-        if (whole) {
-          if (valid) {
-            if (p.out_bf16) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + 32 * c + i) =
-                    make_uint4(bf16x2_rn(o[i] * iv, o[i + 1] * iv), bf16x2_rn(o[i + 2] * iv, o[i + 3] * iv),
-                               bf16x2_rn(o[i + 4] * iv, o[i + 5] * iv), bf16x2_rn(o[i + 6] * iv, o[i + 7] * iv));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + 32 * c + i) =
-                    make_float4(o[i] * iv, o[i + 1] * iv, o[i + 2] * iv, o[i + 3] * iv);
-            }
+          for (int k = 0; k < U; ++k) {
+            const int src = (lane & ~(U - 1)) + k;
+            const int jk = __shfl_sync(0xffffffffu, valid ? j : -1, src), hk = __shfl_sync(0xffffffffu, hq, src);
+            if (jk < 0) continue;
+            const size_t el = ((size_t)jk * p.Hq + hk) * D + wg * kHalf + col;
+            if constexpr (!kHiLo)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + el + unit * 8) = u[k];
+            else
+              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + el + unit * 4) = u[k];
           }
-        } else {
+        };
+        constexpr int kCols = kHiLo || kHalf < 64 ? 32 : 64;  // columns at a time
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += kCols) {
+          float o[kCols];
+#pragma unroll
+          for (int i = 0; i < kCols; i += 32) tmem_ld32(to + c + i, *reinterpret_cast<float(*)[32]>(o + i));
+          tmem_wait_ld();
+          constexpr int U = kHiLo ? 8 : kCols / 8;
+          uint4 u[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            if constexpr (kHiLo)
+              u[i] = make_uint4(__float_as_uint(o[4 * i] * iv), __float_as_uint(o[4 * i + 1] * iv),
+                                __float_as_uint(o[4 * i + 2] * iv), __float_as_uint(o[4 * i + 3] * iv));
+            else
+              u[i] = make_uint4(bf16x2_rn(o[8 * i] * iv, o[8 * i + 1] * iv), bf16x2_rn(o[8 * i + 2] * iv, o[8 * i + 3] * iv),
+                                bf16x2_rn(o[8 * i + 4] * iv, o[8 * i + 5] * iv),
+                                bf16x2_rn(o[8 * i + 6] * iv, o[8 * i + 7] * iv));
+          }
+          put(u, c);
+        }
+      } else {
+        // a record: [D / 4][128 rows] float4, so that neighbouring lanes are neighbours
+        float* rec = reinterpret_cast<float*>(ws + pp.w.oRec) +
+                     (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) * kRows * (D + 2);
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(rec + (size_t)row * D + 32 * c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            *reinterpret_cast<float4*>(rec + ((wg * kHalf + c + i) / 4 * kRows + row) * 4) =
+                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
-      }
-      if (!whole && wg == 0) {
-        rec[kRows * D + row] = M;
-        rec[kRows * D + kRows + row] = lsum;
+        if (wg == 0) {
+          rec[kRows * D + row] = M;
+          rec[kRows * D + kRows + row] = lsum;
+        }
       }
       tc_fence_before();
       mbar_arrive(o_free);
-      named_bar_sync(1, 2 * kWG);  // the statistics are read: the query tile may be rewritten
       first_seg = false;
-    } while (walk_next(pp, rg, w));
+      w = next;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -732,67 +883,83 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   }
 }
 
-// Row blocks that span CTAs, merged in CTA order: a warp per row; the grid runs
-// over the places where the list is cut and the rows, and a row block's first cut
-// has its merge.
+// Row blocks that span CTAs, merged in CTA order.  The grid runs over the places
+// where the list is cut, quarters of 32 rows and 32-column groups; a row block's
+// first cut has its merge.  lane = row; each of the eight warps takes every eighth
+// record, and the eight results are joined in order.
+constexpr int kMergeCols = 32;
 template <int D>
 __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_constant__ Params pp) {
+  constexpr int kQ = kMergeCols / 4, kGroups = D / kMergeCols;
+  __shared__ float s_o[8][32][kMergeCols + 1];
+  __shared__ float s_m[8][32], s_l[8][32];
   const BlockDecodeParams& p = pp.a;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int cut = blockIdx.x / (kRows / 8) + 1, row = (blockIdx.x % (kRows / 8)) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cg = blockIdx.x % kGroups, quarter = blockIdx.x / kGroups % 4, cut = blockIdx.x / (4 * kGroups) + 1;
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const Head h = reinterpret_cast<const Head*>(ws + pp.w.oHead)[cut];
   if (h.rb < 0 || h.first == 0) return;
-  const int64_t r = (int64_t)h.rb * kRows + row;
-  if (r >= (int64_t)p.C * p.G) return;
+  const int row = quarter * 32 + lane, R = p.C * p.G;
+  if (h.rb * kRows + quarter * 32 >= R) return;
   const int grid = pp.w.grid, total = h.total;
   const int a = cut_at(total, grid, cut) - h.first, e = a + h.cnt;
   const int c0 = cta_of(total, grid, a), c1 = cta_of(total, grid, e - 1);
   if (cut != c0 + 1) return;
-  constexpr int E = D / 32;
-  float acc[E], M = -INFINITY, l = 0.f;
+  float4 acc[kQ];
+  float M = -INFINITY, l = 0.f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) acc[i] = 0.f;
-  for (int c = c0; c <= c1; ++c) {
+  for (int i = 0; i < kQ; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0 + warp; c <= c1; c += 8) {
     // a CTA whose range starts inside the row block has it as its first segment
     const int slot = 2 * c + (cut_at(total, grid, c) >= a ? 0 : 1);
     const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)slot * kRows * (D + 2);
-    float x[E];
-    const float* src = rec + (size_t)row * D + lane * E;
-    if constexpr (E == 2) {
-      const float2 t = *reinterpret_cast<const float2*>(src);
-      x[0] = t.x;
-      x[1] = t.y;
-    } else {
+    float4 x[kQ];
 #pragma unroll
-      for (int i = 0; i < E; i += 4) {
-        const float4 t = *reinterpret_cast<const float4*>(src + i);
-        x[i] = t.x;
-        x[i + 1] = t.y;
-        x[i + 2] = t.z;
-        x[i + 3] = t.w;
-      }
-    }
+    for (int i = 0; i < kQ; ++i) x[i] = *reinterpret_cast<const float4*>(rec + ((cg * kQ + i) * kRows + row) * 4);
     const float m = rec[kRows * D + row], ll = rec[kRows * D + kRows + row];
     const float nm = fmaxf(M, m);
     if (nm != -INFINITY) {
       const float f = ex2(M - nm), k = ex2(m - nm);
 #pragma unroll
-      for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + x[i] * k;
+      for (int i = 0; i < kQ; ++i) {
+        acc[i].x = acc[i].x * f + x[i].x * k;
+        acc[i].y = acc[i].y * f + x[i].y * k;
+        acc[i].z = acc[i].z * f + x[i].z * k;
+        acc[i].w = acc[i].w * f + x[i].w * k;
+      }
       l = l * f + ll * k;
       M = nm;
     }
   }
-  const float iv = l > 0.f ? 1.0f / l : 0.f;
-  const size_t o = ((size_t)(r / p.G) * p.Hq + h.kvh * p.G + r % p.G) * D + lane * E;
 #pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    if (p.out_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o + i) = bf16x2_rn(acc[i] * iv, acc[i + 1] * iv);
-    else
-      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + i) = make_float2(acc[i] * iv, acc[i + 1] * iv);
+  for (int i = 0; i < kQ; ++i) {
+    s_o[warp][lane][4 * i] = acc[i].x;
+    s_o[warp][lane][4 * i + 1] = acc[i].y;
+    s_o[warp][lane][4 * i + 2] = acc[i].z;
+    s_o[warp][lane][4 * i + 3] = acc[i].w;
+  }
+  s_m[warp][lane] = M;
+  s_l[warp][lane] = l;
+  __syncthreads();
+  // lane = column now; four rows per warp
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = warp * 4 + i, r = h.rb * kRows + quarter * 32 + rr;
+    if (r >= R) break;
+    float C = -INFINITY, den = 0.f, o = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) C = fmaxf(C, s_m[k][rr]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (s_m[k][rr] == -INFINITY) continue;
+      const float f = ex2(s_m[k][rr] - C);
+      den = __fmaf_rn(s_l[k][rr], f, den);
+      o = __fmaf_rn(s_o[k][rr][lane], f, o);
+    }
+    const float v = den > 0.f ? o / den : 0.f;
+    store_out1(p.out, p.out_bf16, ((size_t)(r / p.G) * p.Hq + h.kvh * p.G + r % p.G) * D + cg * kMergeCols + lane, v);
   }
 }
 
@@ -812,7 +979,7 @@ cudaError_t launch(const Params& pp, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(pp.w.grid), dim3(kThreads), Lay<D>::kTotal, stream, pp);
   if (e != cudaSuccess || pp.w.grid == 1) return e;
-  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * (kRows / 8)), dim3(256), 0, stream, pp);
+  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * 4 * (D / kMergeCols)), dim3(256), 0, stream, pp);
 }
 
 template <int D, bool kHiLo>

@@ -135,6 +135,7 @@ struct BlockReadParams {
   const float* k_scale;
   const float* v_scale;
 };
+constexpr int kCapDeg = 6;
 struct BlockDecodeParams {
   void* out;  // [B, Hq, D]
   int out_bf16;
@@ -154,8 +155,9 @@ struct BlockDecodeParams {
   // B = ceil(C G / 8) groups, HH = Hkv, block_tables one row, seq_lens unused.
   int H, C;
   const int32_t* key_end;    // [C], nullable: one past the last visible key
-  float score_mul;  // q . k -> log2 units (no cap) or twice the tanh's argument in log2 units
+  float score_mul;  // q . k -> the score in log2 units (no cap) or score / cap
   float cap_log2;   // the cap in log2 units, 0: none
+  float cap_poly[kCapDeg + 1];  // cap_log2 tanh(z) = z P(z^2) for |z| <= 1
   void* ws;
   int grid;
 };
