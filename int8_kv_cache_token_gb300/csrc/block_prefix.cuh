@@ -28,10 +28,13 @@
 // third kernel.  So a causal triangle, a window, packed documents and a short
 // chunk over a long history all fill the GPU.
 //
-// Warps: 0 tile copies, 1 MMA issue, 2 tensor memory, 4-7 and 8-11 softmax.  One
+// Warps: 0 tile copies, 1 MMA issue, 2 and 3 query rows (2 also owns the tensor
+// memory), 4-7 and 8-11 softmax.  One
 // thread issues both products: MMAs of a CTA execute in
 // issue order, which is what lets W share its S slot with the S after next.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -103,8 +106,8 @@ struct Lay {
   static constexpr int oL = oM + 2 * kRows * 4;        // the warpgroups' row sums [2][128]
   static constexpr int oSc = oL + 2 * kRows * 4;       // scales of 8 tiles
   static constexpr int oBar = oSc + 8 * kScales * 4;
-  // full[kStages], free[kStages], sc_full[8], s_full[2], p_full[2], m_full[2], pv_done[2], q_full, o_free
-  static constexpr int kBars = 2 * kStages + 8 + 2 + 2 + 2 + 2 + 2;
+  // full[kStages], free[kStages], sc_full[8], s_full[2], p_full[2], m_full[2], pv_done[2], q_full, q_free, o_free
+  static constexpr int kBars = 2 * kStages + 8 + 2 + 2 + 2 + 2 + 3;
   static constexpr int oCtl = oBar + kBars * 8;
   static constexpr int kTotal = oCtl + 16;
   static_assert(kTotal <= 232448, "shared memory");
@@ -287,6 +290,7 @@ __device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, volatile i
 }
 // The same for a whole warp that stays together; false once the CTA has aborted.
 __device__ __forceinline__ bool pwait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   pwait(bar, parity, abort_flag);
   return !__any_sync(0xffffffffu, *abort_flag != 0);
 }
@@ -353,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   uint64_t* m_full = p_full + 2;    // [n & 1] the running maxima after tile n
   uint64_t* pv_done = m_full + 2;   // [n & 1] the product of tile n has joined O
   uint64_t* q_full = pv_done + 2;   // the segment's query rows in shared memory
-  uint64_t* o_free = q_full + 1;    // the segment's O is read
+  uint64_t* q_free = q_full + 1;    // the segment's products have read them
+  uint64_t* o_free = q_free + 1;    // the segment's O is read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::oCtl);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::oCtl + 4);
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
@@ -372,7 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
       mbar_init(&m_full[i], kWG);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_full, 2 * kWG);
+    mbar_init(q_full, 64);
+    mbar_init(q_free, 1);
     mbar_init(o_free, 2 * kWG);
     *abort_flag = 0;
     fence_mbar_init();
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         }
       };
       // a K = 16 step is 32 bytes of a 128-byte row; the descriptors count 16-byte units
-      auto qk = [&](int m) {  // S of the CTA's tile m
+      auto qk = [&](int m, bool end) {  // S of the CTA's tile m; end: the segment's last
 #pragma unroll
         for (int h = 0; h < Ly::kParts; ++h) {
           if (ok) ok = pwait_warp(&full[st], lap & 1, abort_flag);
@@ -537,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
             }
             umma_commit(&free_[st]);
             if (h == Ly::kParts - 1) umma_commit(&s_full[m & 1]);
+            if (h == Ly::kParts - 1 && end) umma_commit(q_free);
           }
           __syncwarp();
           next_stage();
@@ -546,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
       };
       do {
         ok = pwait_warp(q_full, seg & 1, abort_flag);
-        qk(n);
+        if (ok) qk(n, w.len == 1);
         for (int t = 0; t < w.len && ok; ++t, ++n) {
-          if (t + 1 < w.len) qk(n + 1);
+          if (t + 1 < w.len) qk(n + 1, t + 2 == w.len);
           if (ok) ok = pwait_warp(&p_full[n & 1], (n >> 1) & 1, abort_flag);
           if (ok && t == 0 && seg > 0) ok = pwait_warp(o_free, (seg - 1) & 1, abort_flag);
 #pragma unroll
@@ -581,6 +588,32 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         ++seg;
       } while (ok && walk_next(pp, rg, w));
       if (last) mbar_wait(last, last_par);  // every MMA has completed before tensor memory is released
+    } else if (u0 < u1) {
+      // ================= query rows (warps 2 and 3): whole rows by neighbouring lanes =================
+      constexpr int kLanes = D / 8, kAt = 64 / kLanes;  // threads per row, rows at once
+      const int c = (tid - 64) % kLanes, row0 = (tid - 64) / kLanes;
+      const int R = p.C * p.G;
+      int seg = 0;
+      bool ok = true;
+      do {
+        const int r0 = w.rb * kRows + row0;
+        int j = r0 / p.G, h = r0 % p.G;
+        if (seg > 0) ok = pwait_warp(q_free, (seg - 1) & 1, abort_flag);
+        for (int i = 0; i < kRows; i += kAt) {
+          const bool in = r0 + i < R;
+          const uint16_t* src = p.q + (in ? (int64_t)j * p.q_stride + (size_t)(w.kvh * p.G + h) * D + c * 8 : 0);
+          cp_async_16(smem + Ly::oQ + (c / 8) * (kRows * 128) + swz(row0 + i, c % 8), src, in ? 16u : 0u);
+          h += kAt;
+          while (h >= p.G) {
+            h -= p.G;
+            ++j;
+          }
+        }
+        cp_async_wait_all();
+        fence_async_smem();
+        mbar_arrive(q_full);
+        ++seg;
+      } while (ok && walk_next(pp, rg, w));
     }
     __syncwarp();
   } else {
@@ -592,43 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
     float* mref = reinterpret_cast<float*>(smem + Ly::oM);
     float* lrow = reinterpret_cast<float*>(smem + Ly::oL);
     const int R = p.C * p.G;
-    // The query rows of a segment: 16 rows per warp, whole rows by neighbouring
-    // lanes, held in registers until the previous segment's products have read
-    // the tile in shared memory.
-    constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // lanes per row, rows per load
-    constexpr int kLoads = 16 / kAt;
-    uint4 qv[kLoads];
-    const int qrow0 = (warp - kSoftWarp) * 16 + lane / kLanes;
-    auto load_q = [&](const Walk& x) {
-      const int r = x.rb * kRows + qrow0;
-      int j = r / p.G, h = r % p.G;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        qv[i] = make_uint4(0, 0, 0, 0);
-        if (r + i * kAt < R)
-          qv[i] = __ldg(reinterpret_cast<const uint4*>(p.q + (int64_t)j * p.q_stride + (size_t)(x.kvh * p.G + h) * D) +
-                        lane % kLanes);
-        h += kAt;
-        while (h >= p.G) {
-          h -= p.G;
-          ++j;
-        }
-      }
-    };
-    auto store_q = [&]() {
-      const int c = lane % kLanes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        *reinterpret_cast<uint4*>(smem + Ly::oQ + (c / 8) * (kRows * 128) + swz(qrow0 + i * kAt, c % 8)) = qv[i];
-      fence_async_smem();
-      mbar_arrive(q_full);
-    };
     int n = 0;
     bool first_seg = true, more = u0 < u1;
-    if (more) {
-      load_q(w);
-      store_q();
-    }
     while (more) {
       const int r = w.rb * kRows + row;
       const bool valid = r < R;
@@ -661,36 +659,43 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         };
         // u = score log2 e (+ bias) + log2 sV
         if constexpr (kCap) {
-          // z = score / cap; cap log2 e tanh z = z P(z^2) for |z| <= 1: P interpolates
-          // tanh(z) / z at Chebyshev nodes (5e-8 relative), on the FMA pipes that the
-          // exponentials leave idle
-          float ymax = 0.f;
+          // z = score / cap; cap log2 e tanh z = z P(z^2), on the FMA pipes that the
+          // exponentials leave idle: P interpolates tanh(z) / z at Chebyshev nodes, of
+          // degree 3 for |z| <= 1/2 (6e-7 relative; bf16 outputs) or 6 for |z| <= 1 (5e-8)
+          float zmax = 0.f;
 #pragma unroll
           for (int b = 0; b < kBlk; ++b) {
             const uint64_t ks2 = f2(sc[b], sc[b]);
 #pragma unroll
             for (int i = b * kBS; i < (b + 1) * kBS; i += 2) {
-              const uint64_t z = mul2(f2(v[i], v[i + 1]), ks2), y = mul2(z, z);
-              float y0, y1;
-              f2_split(y, y0, y1);
-              ymax = max3(ymax, y0, y1);
-              uint64_t a = f2(p.cap_poly[kCapDeg], p.cap_poly[kCapDeg]);
-#pragma unroll
-              for (int d = kCapDeg - 1; d >= 0; --d) a = fma2(a, y, f2(p.cap_poly[d], p.cap_poly[d]));
-              f2_split(fma2(a, z, f2(addend(b, i - b * kBS), addend(b, i + 1 - b * kBS))), v[i], v[i + 1]);
+              f2_split(mul2(f2(v[i], v[i + 1]), ks2), v[i], v[i + 1]);
+              zmax = max3(zmax, fabsf(v[i]), fabsf(v[i + 1]));
             }
           }
-          if (__any_sync(0xffffffffu, !(ymax <= 1.f))) {  // some score above the cap: 1 - 2 / (e^2z + 1)
+          auto poly = [&](auto deg, const float* coef) {
+            constexpr int N = decltype(deg)::value;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
-            tmem_wait_ld();
+            for (int b = 0; b < kBlk; ++b)
 #pragma unroll
-            for (int b = 0; b < kBlk; ++b) {
-              const float ks = sc[b] * (2.f * kLog2e);
+              for (int i = b * kBS; i < (b + 1) * kBS; i += 2) {
+                const uint64_t z = f2(v[i], v[i + 1]), y = mul2(z, z);
+                uint64_t a = f2(coef[N], coef[N]);
+#pragma unroll
+                for (int d = N - 1; d >= 0; --d) a = fma2(a, y, f2(coef[d], coef[d]));
+                f2_split(fma2(a, z, f2(addend(b, i - b * kBS), addend(b, i + 1 - b * kBS))), v[i], v[i + 1]);
+              }
+          };
+          if (!kHiLo && __all_sync(0xffffffffu, zmax <= 0.5f)) {
+            poly(std::integral_constant<int, 3>{}, p.cap_poly3);
+          } else if (__all_sync(0xffffffffu, zmax <= 1.f)) {
+            poly(std::integral_constant<int, kCapDeg>{}, p.cap_poly);
+          } else {  // some score above the cap: 1 - 2 / (e^2z + 1)
+#pragma unroll
+            for (int b = 0; b < kBlk; ++b)
 #pragma unroll
               for (int i = b * kBS; i < (b + 1) * kBS; ++i)
-                v[i] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(v[i] * ks) + 1.f), p.cap_log2 + addend(b, i - b * kBS));
-            }
+                v[i] = __fmaf_rn(-2.f * p.cap_log2, rcp_approx(ex2(v[i] * (2.f * kLog2e)) + 1.f),
+                                 p.cap_log2 + addend(b, i - b * kBS));
           }
         } else {
 #pragma unroll
@@ -708,14 +713,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
             for (int i = 0; i < kKeys; ++i) v[i] = __fmaf_rn(2.f * slope, fmaxf(d0 + (float)i, 0.f), v[i]);
           }
         }
-        if (!__all_sync(0xffffffffu, key0 >= lo && key0 + kKeys <= hi)) {  // hidden keys: 32 at a time as bits
+        // hidden keys
+        if (__any_sync(0xffffffffu, key0 + kKeys > hi)) {
+          const int e = hi - key0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int a = max(0, min(32, lo - key0 - 32 * c)), e = max(0, min(32, hi - key0 - 32 * c));
-            const uint32_t seen = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & ~(a == 32 ? 0xffffffffu : (1u << a) - 1u);
+          for (int i = 0; i < kKeys; ++i) v[i] = i < e ? v[i] : -INFINITY;
+        }
+        if (__any_sync(0xffffffffu, key0 < lo)) {
+          const int a = lo - key0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[32 * c + i] = (seen >> i) & 1u ? v[32 * c + i] : -INFINITY;
-          }
+          for (int i = 0; i < kKeys; ++i) v[i] = i >= a ? v[i] : -INFINITY;
         }
         float mb[8];
 #pragma unroll
@@ -792,16 +799,14 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         tc_fence_before();
         mbar_arrive(&p_full[n & 1]);
       }
-      // ---- the end of the segment: O / l, or a record.  The next segment's query
-      // rows are on their way meanwhile, and its first product may start before O is read.
+      // ---- the end of the segment: O / l, or a record.  The next segment's first
+      // product may start before O is read.
       const int last = n - 1;
       Walk next = w;
       more = walk_next(pp, rg, next);
-      if (more) load_q(next);
       named_bar_sync(1, 2 * kWG);  // both warpgroups are through their tiles: S(last) was complete
       const float M = mref[(last & 1) * kRows + row];
       lrow[wg * kRows + row] = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
-      if (more) store_q();
       named_bar_sync(1, 2 * kWG);
       const float lsum = lrow[row] + lrow[kRows + row];
       pwait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);

@@ -153,6 +153,14 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src, uint32_t 
                : "memory");
 }
 
+// The same for 16 bytes, past L1; both addresses 16-byte aligned.
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+// Waits for every cp.async of this thread.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The mbarrier's current phase also waits for every cp.async this thread has
 // issued so far (the pending count is raised by one now and lowered when the
 // copies land, so the barrier's expected arrival count is unchanged).

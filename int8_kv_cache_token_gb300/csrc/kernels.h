@@ -158,6 +158,7 @@ struct BlockDecodeParams {
   float score_mul;  // q . k -> the score in log2 units (no cap) or score / cap
   float cap_log2;   // the cap in log2 units, 0: none
   float cap_poly[kCapDeg + 1];  // cap_log2 tanh(z) = z P(z^2) for |z| <= 1
+  float cap_poly3[4];           // the same for |z| <= 1/2
   void* ws;
   int grid;
 };
