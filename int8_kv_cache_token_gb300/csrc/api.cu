@@ -625,6 +625,7 @@ static i8kv_status block_attn_common(i8kv::BlockDecodeParams& p, void* out, int 
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
+  p.divG = i8kv::FastDiv((uint32_t)p.G);
   p.D = D;
   p.num_blocks = num_blocks;
   p.window = window;

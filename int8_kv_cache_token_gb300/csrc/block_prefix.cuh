@@ -8,16 +8,19 @@
 // O = sum w cV / sum w / sV, so the two scales of a 16-key block are one multiply
 // and one addend of its 16 scores, and the products below run on the bare codes.
 //
-// A CTA owns 128 rows (token, head) of one KV head at a time and walks 128-key
-// tiles:
+// A CTA owns a row block, 128 (token, head) rows of one KV head (256 for head_dim
+// up to 128), and walks 128-key tiles:
 //   S = Q K^T    tcgen05, bf16 Q (as given) x bf16 codes (exact), M = N = 128, K = D
 //   u, M, w      CUDA cores, one thread per row
 //   O += W V     tcgen05, f16 W (from tensor memory) x f16 codes (exact), N = D
-// S has two slots in tensor memory, so the softmax of one tile runs beside the
-// products of its neighbours; two warpgroups take alternate tiles and hand the
-// running maximum on.  W overwrites its S slot.  O stays in tensor memory and is
-// rescaled only when a row's maximum grows by more than 2^8.  For an fp32 output W
-// is two f16 parts (2^-22 instead of 2^-12 relative), side by side in the slot.
+// S has two slots in tensor memory, so that one softmax runs beside the products
+// of the other.  W overwrites its S slot.  With head_dim up to 128 the two are
+// two 128-row halves of the row block, each with its warpgroup, S and O: every
+// K / V tile that is loaded serves 256 rows.  A head_dim of 256 leaves room for one
+// O: two warpgroups take alternate tiles of the same 128 rows and hand the running
+// maximum on.  O is rescaled only when a row's maximum grows by more than 2^8.  For
+// an fp32 output W is two f16 parts (2^-22 instead of 2^-12 relative), side by side
+// in the slot.
 //
 // The codes become 16-bit operand tiles once per call (block_tiles_kernel), in
 // the swizzled layout that the MMAs read, so a tile is one bulk copy per half and
@@ -28,8 +31,8 @@
 // third kernel.  So a causal triangle, a window, packed documents and a short
 // chunk over a long history all fill the GPU.
 //
-// Warps: 0 tile copies, 1 MMA issue, 2 and 3 query rows (2 also owns the tensor
-// memory), 4-7 and 8-11 softmax.  One
+// Warps: 0 tile copies, 1 MMA issue, 2 tensor memory, 4-7 and 8-11 softmax (and
+// the query rows).  One
 // thread issues both products: MMAs of a CTA execute in
 // issue order, which is what lets W share its S slot with the S after next.
 #pragma once
@@ -43,7 +46,9 @@ namespace i8kv {
 namespace bp {
 
 constexpr int kBS = 16;
-constexpr int kRows = 128;
+constexpr int kRows = 128;          // rows of one MMA: one per tensor-memory lane
+__host__ __device__ constexpr bool paired(int D) { return D <= 128; }
+__host__ __device__ constexpr int block_rows(int D) { return paired(D) ? 2 * kRows : kRows; }
 constexpr int kKeys = 128;
 constexpr int kBlk = kKeys / kBS;  // cache blocks per tile
 constexpr int kThreads = 384;
@@ -73,7 +78,8 @@ struct Plan {
 inline Plan plan_of(int H, int C, int G, int Hkv, int D, int window, int grid) {
   Plan p;
   auto up = [](size_t x) { return (x + 127) / 128 * 128; };
-  p.nrb = (int)(((int64_t)C * G + kRows - 1) / kRows);
+  const int rows = block_rows(D);
+  p.nrb = (int)(((int64_t)C * G + rows - 1) / rows);
   p.tile0 = window > 0 && H - window + 1 > 0 ? (H - window + 1) / kKeys : 0;  // no row sees an earlier key
   p.ntiles = (H + C + kKeys - 1) / kKeys - p.tile0;
   p.grid = grid;
@@ -84,7 +90,7 @@ inline Plan plan_of(int H, int C, int G, int Hkv, int D, int window, int grid) {
   p.oK = p.oScale + up(n * kScales * 4);
   p.oV = p.oK + n * tile;
   p.oRec = p.oV + n * tile;
-  p.bytes = p.oRec + (size_t)2 * grid * kRows * (D + 2) * 4;
+  p.bytes = p.oRec + (size_t)2 * grid * rows * (D + 2) * 4;
   return p;
 }
 
@@ -95,23 +101,26 @@ struct Params {
 
 template <int D>
 struct Lay {
-  static constexpr int kParts = D == 64 ? 1 : 2;       // stages per operand tile
+  static constexpr bool kPair = paired(D);
+  static constexpr int kRB = block_rows(D);            // rows of a row block
+  static constexpr int kParts = D == 256 ? 2 : 1;      // stages per operand tile
   static constexpr int kTile = kKeys * D * 2;
-  static constexpr int kStage = kTile / kParts;        // K: half the dims; V: half the keys
-  static constexpr int kStages = D == 256 ? 5 : D == 128 ? 11 : 12;
-  static constexpr int kQ = kRows * D * 2;
-  static constexpr int oQ = 0;                         // [D/64][128 rows][128 B]
+  static constexpr int kStage = kTile / kParts;        // two parts: K half the dims, V half the keys
+  static constexpr int kStages = D == 64 ? 11 : 5;
+  static constexpr int kQ = kRB * D * 2;
+  static constexpr int oQ = 0;                         // [kRB / 128][D/64][128 rows][128 B]
   static constexpr int oRing = oQ + kQ;
   static constexpr int oM = oRing + kStages * kStage;  // M [2][128]
   static constexpr int oL = oM + 2 * kRows * 4;        // the warpgroups' row sums [2][128]
-  static constexpr int oSc = oL + 2 * kRows * 4;       // scales of 8 tiles
-  static constexpr int oBar = oSc + 8 * kScales * 4;
-  // full[kStages], free[kStages], sc_full[8], s_full[2], p_full[2], m_full[2], pv_done[2], q_full, q_free, o_free
-  static constexpr int kBars = 2 * kStages + 8 + 2 + 2 + 2 + 2 + 3;
+  static constexpr int oSc = oL + 2 * kRows * 4;       // scales of kSc tiles
+  static constexpr int kSc = D == 64 ? 8 : 4;          // a slot is refilled only after its tile's products
+  static constexpr int oBar = oSc + kSc * kScales * 4;
+  // full[kStages], free[kStages], sc_full[kSc], s_full[2], p_full[2][2], m_full[2], pv_done[2], q_full[2], o_free[2]
+  static constexpr int kBars = 2 * kStages + kSc + 2 + 4 + 2 + 2 + 2 + 2;
   static constexpr int oCtl = oBar + kBars * 8;
   static constexpr int kTotal = oCtl + 16;
   static_assert(kTotal <= 232448, "shared memory");
-  static constexpr uint32_t kOCol = 256;
+  static constexpr uint32_t kOCol = 256;  // O; in pairs the second one D columns on
 };
 
 // Byte offset of 16-byte chunk c of row r of a 128-byte-row tile, swizzled.
@@ -141,7 +150,8 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   // row block ranges
   for (int rb = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; rb < pp.w.nrb; rb += gridDim.x * gridDim.y * 8) {
-    const int j0 = (int)((int64_t)rb * kRows / p.G), j1 = min(p.C - 1, (int)(((int64_t)rb * kRows + kRows - 1) / p.G));
+    constexpr int kRB = block_rows(D);
+    const int j0 = rb * kRB / p.G, j1 = min(p.C - 1, (int)(((int64_t)rb * kRB + kRB - 1) / p.G));
     int lo = 0x7fffffff, hi = 0, lo_in = 0, hi_in = 0x7fffffff;
     for (int j = j0 + lane; j <= j1; j += 32) {
       int a, b;
@@ -351,14 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::oBar);
   uint64_t* free_ = full + NS;
-  uint64_t* sc_full = free_ + NS;   // [n % 8] scales of tile n
-  uint64_t* s_full = sc_full + 8;   // [n & 1] S of tile n in tensor memory
-  uint64_t* p_full = s_full + 2;    // [n & 1] W of tile n in tensor memory
-  uint64_t* m_full = p_full + 2;    // [n & 1] the running maxima after tile n
-  uint64_t* pv_done = m_full + 2;   // [n & 1] the product of tile n has joined O
-  uint64_t* q_full = pv_done + 2;   // the segment's query rows in shared memory
-  uint64_t* q_free = q_full + 1;    // the segment's products have read them
-  uint64_t* o_free = q_free + 1;    // the segment's O is read
+  uint64_t* sc_full = free_ + NS;   // [n % kSc] scales of tile n
+  // per S slot (in pairs the warpgroup, else n & 1):
+  uint64_t* s_full = sc_full + Ly::kSc;  // S in tensor memory
+  uint64_t* p_full = s_full + 2;    // W in tensor memory: [slot][keys 0..63, 64..127]
+  uint64_t* m_full = p_full + 4;    // the running maxima after the tile (not in pairs)
+  uint64_t* pv_done = m_full + 2;   // its product has joined O
+  uint64_t* q_full = pv_done + 2;   // the segment's query rows in shared memory (in pairs one per warpgroup)
+  uint64_t* o_free = q_full + 2;    // the segment's O is read (in pairs one per warpgroup)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::oCtl);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::oCtl + 4);
   const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
@@ -370,16 +380,17 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
       mbar_init(&full[i], 1);
       mbar_init(&free_[i], 1);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < Ly::kSc; ++i) mbar_init(&sc_full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], kWG);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kWG);
       mbar_init(&m_full[i], kWG);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_full, 64);
-    mbar_init(q_free, 1);
-    mbar_init(o_free, 2 * kWG);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], kWG);
+      mbar_init(&o_free[i], Ly::kPair ? kWG : 2 * kWG);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -455,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   // row blocks without a visible key: zero rows
   for (int rb = blockIdx.x; rb < pp.w.nrb; rb += grid) {
     if (rg[rb].hi != rg[rb].lo) continue;
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-      const int64_t r = (int64_t)rb * kRows + i / (D / 4);
+    for (int i = tid; i < Ly::kRB * (D / 4); i += kThreads) {
+      const int64_t r = (int64_t)rb * Ly::kRB + i / (D / 4);
       if (r < (int64_t)p.C * p.G)
         for (int k = 0; k < p.Hkv; ++k)
           store_out4(p.out, p.out_bf16, ((size_t)(r / p.G) * p.Hq + k * p.G + r % p.G) * D + (i % (D / 4)) * 4,
@@ -483,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
             bulk_g2s(smem + Ly::oRing + st * Ly::kStage, src[which] + ti * Ly::kTile + h * Ly::kStage, Ly::kStage, &full[st]);
             mbar_arrive(&full[st]);
             if (which == 0 && h == 0) {
-              uint64_t* b = &sc_full[n % 8];
+              uint64_t* b = &sc_full[n % Ly::kSc];
               mbar_expect_tx(b, kScales * 4);
-              bulk_g2s(smem + Ly::oSc + (n % 8) * kScales * 4, scl + ti * kScales, kScales * 4, b);
+              bulk_g2s(smem + Ly::oSc + (n % Ly::kSc) * kScales * 4, scl + ti * kScales, kScales * 4, b);
               mbar_arrive(b);
             }
           }
@@ -501,14 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
       do {
         const size_t t0 = (size_t)w.kvh * pp.w.ntiles + (w.lo + w.first - pp.w.tile0);
         load(0, t0);
-        for (int t = 0; t < w.len && ok; ++t) {
+        for (int t = 0; t < w.len && ok; ++t) {  // in the order of their use
+          if (Ly::kPair) load(1, t0 + t);
           if (t + 1 < w.len) load(0, t0 + t + 1);
-          load(1, t0 + t);
+          if (!Ly::kPair) load(1, t0 + t);
         }
       } while (ok && walk_next(pp, rg, w));
       if (!ok) {  // copies under way land before the CTA exits
         for (int k = max(0, c - NS); k < c; ++k) mbar_wait(&full[k % NS], (k / NS) & 1);
-        for (int k = max(0, n - 7); k <= n; ++k) mbar_wait(&sc_full[k % 8], (k / 8) & 1);
+        for (int k = max(0, n + 1 - Ly::kSc); k <= n; ++k) mbar_wait(&sc_full[k % Ly::kSc], (k / Ly::kSc) & 1);
       }
     } else if (u0 < u1 && warp == 1) {
       // ================= MMA issue =================
@@ -526,7 +538,90 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         }
       };
       // a K = 16 step is 32 bytes of a 128-byte row; the descriptors count 16-byte units
-      auto qk = [&](int m, bool end) {  // S of the CTA's tile m; end: the segment's last
+      if constexpr (Ly::kPair) {
+        // S of rows 128 g .. + 127 of the row block from the K stage at kd, and O += W V
+        auto qk_half = [&](int g, uint64_t kd) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            umma_f16(tmem + g * kKeys, qdesc + g * (kRows * D / 8) + (k / 4) * (kRows * 8) + (k % 4) * 2,
+                     kd + (k / 4) * (kKeys * 8) + (k % 4) * 2, idesc_qk, k > 0);
+          umma_commit(&s_full[g]);
+        };
+        auto pv_half = [&](int g, int half, uint64_t vd, bool add) {  // the tile's keys 64 half .. + 63
+#pragma unroll
+          for (int k = 4 * half; k < 4 * half + 4; ++k) {
+            const uint64_t b = vd + (k / 4) * (D * 8) + (k % 4) * 2;
+            umma_f16_ta(tmem + Ly::kOCol + g * D, tmem + g * kKeys + k * 8, b, idesc_pv, add || k > 0);
+            if constexpr (kHiLo) umma_f16_ta(tmem + Ly::kOCol + g * D, tmem + g * kKeys + 64 + k * 8, b, idesc_pv, true);
+          }
+          if (half) umma_commit(&pv_done[g]);
+        };
+        int n2 = 0, seg2 = 0;  // tiles and segments of the second warpgroup
+        do {
+          const bool two = w.rb * Ly::kRB + kRows < p.C * p.G;
+          ok = pwait_warp(&q_full[0], seg & 1, abort_flag) && (!two || pwait_warp(&q_full[1], seg2 & 1, abort_flag)) &&
+               pwait_warp(&full[st], lap & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t kd = rdesc + (uint64_t)(st * (Ly::kStage / 16));
+            qk_half(0, kd);
+            if (two) qk_half(1, kd);
+            umma_commit(&free_[st]);
+          }
+          __syncwarp();
+          next_stage();
+          for (int t = 0; t < w.len; ++t) {
+            const bool more = t + 1 < w.len;
+            const int vs = st, ks = st + 1 == NS ? 0 : st + 1, klap = st + 1 == NS ? lap + 1 : lap;
+            const uint64_t vd = rdesc + (uint64_t)(vs * (Ly::kStage / 16)), kd = rdesc + (uint64_t)(ks * (Ly::kStage / 16));
+            ok = pwait_warp(&full[vs], lap & 1, abort_flag) && (!more || pwait_warp(&full[ks], klap & 1, abort_flag)) &&
+                 (t > 0 || seg == 0 || pwait_warp(&o_free[0], (seg - 1) & 1, abort_flag)) &&
+                 pwait_warp(&p_full[0], n & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) pv_half(0, 0, vd, t > 0);
+            __syncwarp();
+            ok = pwait_warp(&p_full[1], n & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              pv_half(0, 1, vd, true);
+              if (more) qk_half(0, kd);
+            }
+            __syncwarp();
+            if (two) {
+              ok = (t > 0 || seg2 == 0 || pwait_warp(&o_free[1], (seg2 - 1) & 1, abort_flag)) &&
+                   pwait_warp(&p_full[2], n2 & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) pv_half(1, 0, vd, t > 0);
+              __syncwarp();
+              ok = pwait_warp(&p_full[3], n2 & 1, abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (elect_one()) {
+              if (two) pv_half(1, 1, vd, true);
+              umma_commit(&free_[vs]);
+              if (more) {
+                if (two) qk_half(1, kd);
+                umma_commit(&free_[ks]);
+              }
+              last = &free_[more ? ks : vs];
+              last_par = (more ? klap : lap) & 1;
+            }
+            __syncwarp();
+            next_stage();
+            if (more) next_stage();
+            ++n;
+            n2 += two;
+          }
+          ++seg;
+          seg2 += two;
+        } while (ok && walk_next(pp, rg, w));
+      } else {
+      auto qk = [&](int m) {  // S of the CTA's tile m
 #pragma unroll
         for (int h = 0; h < Ly::kParts; ++h) {
           if (ok) ok = pwait_warp(&full[st], lap & 1, abort_flag);
@@ -543,7 +638,6 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
             }
             umma_commit(&free_[st]);
             if (h == Ly::kParts - 1) umma_commit(&s_full[m & 1]);
-            if (h == Ly::kParts - 1 && end) umma_commit(q_free);
           }
           __syncwarp();
           next_stage();
@@ -552,15 +646,15 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         last_par = (m >> 1) & 1;
       };
       do {
-        ok = pwait_warp(q_full, seg & 1, abort_flag);
-        if (ok) qk(n, w.len == 1);
+        ok = pwait_warp(&q_full[0], seg & 1, abort_flag);
+        if (ok) qk(n);
         for (int t = 0; t < w.len && ok; ++t, ++n) {
-          if (t + 1 < w.len) qk(n + 1, t + 2 == w.len);
-          if (ok) ok = pwait_warp(&p_full[n & 1], (n >> 1) & 1, abort_flag);
-          if (ok && t == 0 && seg > 0) ok = pwait_warp(o_free, (seg - 1) & 1, abort_flag);
+          if (t + 1 < w.len) qk(n + 1);
+          if (ok && t == 0 && seg > 0) ok = pwait_warp(&o_free[0], (seg - 1) & 1, abort_flag);
 #pragma unroll
-          for (int h = 0; h < Ly::kParts; ++h) {
+          for (int h = 0; h < Ly::kParts; ++h) {  // the two halves of the keys, as their weights arrive
             if (ok) ok = pwait_warp(&full[st], lap & 1, abort_flag);
+            if (ok) ok = pwait_warp(&p_full[2 * (n & 1) + h], (n >> 1) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             constexpr int kSteps = kKeys / 16 / Ly::kParts;
@@ -587,65 +681,87 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         }
         ++seg;
       } while (ok && walk_next(pp, rg, w));
+      }
       if (last) mbar_wait(last, last_par);  // every MMA has completed before tensor memory is released
-    } else if (u0 < u1) {
-      // ================= query rows (warps 2 and 3): whole rows by neighbouring lanes =================
-      constexpr int kLanes = D / 8, kAt = 64 / kLanes;  // threads per row, rows at once
-      const int c = (tid - 64) % kLanes, row0 = (tid - 64) / kLanes;
-      const int R = p.C * p.G;
-      int seg = 0;
-      bool ok = true;
-      do {
-        const int r0 = w.rb * kRows + row0;
-        int j = r0 / p.G, h = r0 % p.G;
-        if (seg > 0) ok = pwait_warp(q_free, (seg - 1) & 1, abort_flag);
-        for (int i = 0; i < kRows; i += kAt) {
-          const bool in = r0 + i < R;
-          const uint16_t* src = p.q + (in ? (int64_t)j * p.q_stride + (size_t)(w.kvh * p.G + h) * D + c * 8 : 0);
-          cp_async_16(smem + Ly::oQ + (c / 8) * (kRows * 128) + swz(row0 + i, c % 8), src, in ? 16u : 0u);
-          h += kAt;
-          while (h >= p.G) {
-            h -= p.G;
-            ++j;
-          }
-        }
-        cp_async_wait_all();
-        fence_async_smem();
-        mbar_arrive(q_full);
-        ++seg;
-      } while (ok && walk_next(pp, rg, w));
     }
     __syncwarp();
   } else {
-    // ================= softmax: a thread per row, the warpgroups on alternate tiles =================
+    // ================= softmax: a thread per row =================
+    // In pairs each warpgroup has 128 rows, a slot of S and an O of its own and takes
+    // every tile; else both have the same rows and take alternate tiles.
     regs_inc<kRegsSoft>();
     const int wg = (warp - kSoftWarp) >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to0 = trow + Ly::kOCol + (Ly::kPair ? wg * D : 0);  // this row of O
     float* mref = reinterpret_cast<float*>(smem + Ly::oM);
     float* lrow = reinterpret_cast<float*>(smem + Ly::oL);
     const int R = p.C * p.G;
-    int n = 0;
+    // The query rows of a segment's row block (in pairs of this warpgroup's half):
+    // whole rows by neighbouring lanes, asked for as soon as the previous segment's
+    // last S is complete, that is, once its products have read the old rows.
+    auto ask_q = [&](const Walk& x) {
+      constexpr int kLanes = D / 8, kAt = kWG / kLanes;  // threads per row, rows at once
+      const int c = (tid & (kWG - 1)) % kLanes, row0 = (tid & (kWG - 1)) / kLanes;
+      const int r0 = x.rb * Ly::kRB + (Ly::kPair ? wg * kRows : 0) + row0;
+      uint8_t* dst = smem + Ly::oQ + (Ly::kPair ? wg * (kRows * D * 2) : 0) + (c / 8) * (kRows * 128);
+#pragma unroll 4
+      for (int i = 0; i < kRows; i += kAt) {
+        const int r = r0 + i, j = p.divG.div(r), h = r - j * p.G;
+        const bool in = r < R;
+        const uint16_t* src = p.q + (in ? (int64_t)j * p.q_stride + (size_t)(x.kvh * p.G + h) * D + c * 8 : 0);
+        cp_async_16(dst + swz(row0 + i, c % 8), src, in ? 16u : 0u);
+      }
+    };
+    auto hand_q = [&]() {
+      cp_async_wait_all();
+      fence_async_smem();
+      mbar_arrive(&q_full[Ly::kPair ? wg : 0]);
+    };
+    auto has_rows = [&](const Walk& x) { return !Ly::kPair || x.rb * Ly::kRB + wg * kRows < R; };
+    int n = 0, tile = 0;  // this warpgroup's tiles in pairs, else the CTA's; the CTA's
     bool first_seg = true, more = u0 < u1;
+    if (more && has_rows(w) && (Ly::kPair || wg == 0)) {
+      ask_q(w);
+      hand_q();
+    }
     while (more) {
-      const int r = w.rb * kRows + row;
+      Walk next = w;
+      more = walk_next(pp, rg, next);
+      if (!has_rows(w)) {  // the last row block may have rows for one warpgroup only
+        if (more && has_rows(next)) {
+          ask_q(next);
+          hand_q();
+        }
+        tile += w.len;
+        first_seg = false;
+        w = next;
+        continue;
+      }
+      const int r = w.rb * Ly::kRB + (Ly::kPair ? wg * kRows : 0) + row;
       const bool valid = r < R;
-      const int j = valid ? r / p.G : 0, hq = w.kvh * p.G + (valid ? r % p.G : 0);
+      const int j = valid ? p.divG.div(r) : 0, hq = w.kvh * p.G + (valid ? r - j * p.G : 0);
       int lo = 0, hi = 0;
       if (valid) interval(p, j, lo, hi);
       const int pos = p.H + j;
       float slope = 0.f;
       if constexpr (kSlope) slope = valid ? -__ldg(p.slopes + hq) * kLog2e : 0.f;
+      bool asked = false;
       float l = 0.f, Mown = -INFINITY;
-      for (int t = 0; t < w.len; ++t, ++n) {
-        if ((n & 1) != wg) continue;
+      for (int t = 0; t < w.len; ++t, ++n, ++tile) {
+        if (!Ly::kPair && (n & 1) != wg) continue;
         const int key0 = (w.lo + w.first + t) * kKeys;
-        pwait(&sc_full[n % 8], (n / 8) & 1, abort_flag);
-        const float* sc = reinterpret_cast<const float*>(smem + Ly::oSc) + (n % 8) * kScales;
-        pwait(&s_full[n & 1], (n >> 1) & 1, abort_flag);
+        const int slot = Ly::kPair ? wg : n & 1, phase = Ly::kPair ? n & 1 : (n >> 1) & 1;
+        pwait(&s_full[slot], phase, abort_flag);
+        pwait(&sc_full[tile % Ly::kSc], (tile / Ly::kSc) & 1, abort_flag);  // landed before S
+        if (t + 1 == w.len && more && has_rows(next)) {
+          ask_q(next);
+          asked = true;
+        }
+        const float* sc = reinterpret_cast<const float*>(smem + Ly::oSc) + (tile % Ly::kSc) * kScales;
         __syncwarp();
         tc_fence_after();
-        const uint32_t ts = trow + (n & 1) * kKeys;
+        const uint32_t ts = trow + slot * kKeys;
         float v[kKeys];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
@@ -733,9 +849,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
           mb[b] = fmaxf(mb[b], v[b * 16 + 15]);
         }
         const float mx = fmaxf(max3(max3(mb[0], mb[1], mb[2]), mb[3], mb[4]), max3(mb[5], mb[6], mb[7]));
-        // the running maximum: from the neighbour's tile, to the neighbour's next
-        float M = -INFINITY;
-        if (t > 0) {
+        // the running maximum: this thread's own in pairs, else from the neighbour's
+        // tile and on to the neighbour's next
+        float M = Ly::kPair ? Mown : -INFINITY;
+        if (!Ly::kPair && t > 0) {
           pwait(&m_full[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag);
           M = mref[((n - 1) & 1) * kRows + row];
         }
@@ -744,18 +861,35 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
           if (M != -INFINITY) alpha = ex2(M - mx);
           M = mx;
         }
-        mref[(n & 1) * kRows + row] = M;
-        mbar_arrive(&m_full[n & 1]);
+        if constexpr (!Ly::kPair) {
+          mref[(n & 1) * kRows + row] = M;
+          mbar_arrive(&m_full[n & 1]);
+        }
         const float m0 = M == -INFINITY ? 0.f : M;  // a row that has seen no key yet
         if (Mown != M) {
           l = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
           Mown = M;
         }
         __syncwarp();
-        uint32_t pk[32], pl[kHiLo ? 32 : 1];
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // rare: O joins the new maximum
+          pwait(&pv_done[Ly::kPair ? wg : (n - 1) & 1], Ly::kPair ? (n - 1) & 1 : ((n - 1) >> 1) & 1, abort_flag);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            uint32_t ob[32];
+            tmem_ld32(to0 + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ob[i] = __float_as_uint(o[i] * alpha);
+            tmem_st32(to0 + 32 * c, ob);
+          }
+        }
         const uint64_t nm = f2(-m0, -m0);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32], pl[kHiLo ? 32 : 1];
 #pragma unroll
           for (int b = 4 * half; b < 4 * half + 4; ++b) {
             uint64_t sum = 0;
@@ -779,60 +913,53 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
           __syncwarp();
           tmem_st32(ts + 32 * half, pk);
           if constexpr (kHiLo) tmem_st32(ts + 64 + 32 * half, pl);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * slot + half]);
         }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // rare: O joins the new maximum
-          pwait(&pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag);
-          __syncwarp();
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float o[32];
-            uint32_t ob[32];
-            tmem_ld32(trow + Ly::kOCol + 32 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ob[i] = __float_as_uint(o[i] * alpha);
-            tmem_st32(trow + Ly::kOCol + 32 * c, ob);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[n & 1]);
       }
       // ---- the end of the segment: O / l, or a record.  The next segment's first
       // product may start before O is read.
+      if (asked) hand_q();
       const int last = n - 1;
-      Walk next = w;
-      more = walk_next(pp, rg, next);
-      named_bar_sync(1, 2 * kWG);  // both warpgroups are through their tiles: S(last) was complete
-      const float M = mref[(last & 1) * kRows + row];
-      lrow[wg * kRows + row] = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
-      named_bar_sync(1, 2 * kWG);
-      const float lsum = lrow[row] + lrow[kRows + row];
-      pwait(&pv_done[last & 1], (last >> 1) & 1, abort_flag);
+      float M = Mown, lsum = l;
+      if constexpr (!Ly::kPair) {
+        named_bar_sync(1, 2 * kWG);  // both warpgroups are through their tiles: S(last) was complete
+        M = mref[(last & 1) * kRows + row];
+        lrow[wg * kRows + row] = Mown == -INFINITY ? 0.f : l * ex2(Mown - M);
+        named_bar_sync(1, 2 * kWG);
+        lsum = lrow[row] + lrow[kRows + row];
+      }
+      pwait(&pv_done[Ly::kPair ? wg : last & 1], Ly::kPair ? last & 1 : (last >> 1) & 1, abort_flag);
       __syncwarp();
       tc_fence_after();
-      constexpr int kHalf = D / 2;  // columns per warpgroup
-      const uint32_t to = trow + Ly::kOCol + wg * kHalf;
+      constexpr int kHalf = Ly::kPair ? D : D / 2;  // columns per warpgroup
+      const int col0 = Ly::kPair ? 0 : wg * kHalf;
+      const uint32_t to = to0 + col0;
       if (w.first == 0 && w.len == w.cnt) {
         const float iv = lsum > 0.f ? 1.0f / lsum : 0.f;
         // 16-byte units, brought to whole 128-byte lines of a row by transposing
         // among eight lanes (four for 64 bytes): a row per lane costs 32 lines a store
-        auto put = [&](auto& u, int col) {  // U units from column `col` of this warpgroup's half
+        constexpr int kG = kHiLo || kHalf >= 64 ? 8 : 4;  // lanes, and rows, of a group
+        size_t at[kG];
+        {
+          const size_t mine = valid ? ((size_t)j * p.Hq + hq) * D + col0 : ~(size_t)0;
+#pragma unroll
+          for (int k = 0; k < kG; ++k) at[k] = __shfl_sync(0xffffffffu, (unsigned long long)mine, (lane & ~(kG - 1)) + k);
+        }
+        auto put = [&](auto& u, int col) {  // units from column `col` of this warpgroup's part
           constexpr int U = sizeof(u) / 16;
+          static_assert(U == kG, "");
           transpose_units<U>(u, lane);
           const int unit = lane % U;
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int src = (lane & ~(U - 1)) + k;
-            const int jk = __shfl_sync(0xffffffffu, valid ? j : -1, src), hk = __shfl_sync(0xffffffffu, hq, src);
-            if (jk < 0) continue;
-            const size_t el = ((size_t)jk * p.Hq + hk) * D + wg * kHalf + col;
-            if constexpr (!kHiLo)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + el + unit * 8) = u[k];
-            else
-              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + el + unit * 4) = u[k];
-          }
+          for (int k = 0; k < U; ++k)
+            if (at[k] != ~(size_t)0) {
+              if constexpr (!kHiLo)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at[k] + col + unit * 8) = u[k];
+              else
+                *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at[k] + col + unit * 4) = u[k];
+            }
         };
         constexpr int kCols = kHiLo || kHalf < 64 ? 32 : 64;  // columns at a time
 #pragma unroll 1
@@ -856,9 +983,10 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
           put(u, c);
         }
       } else {
-        // a record: [D / 4][128 rows] float4, so that neighbouring lanes are neighbours
+        // a record: [D / 4][rows] float4, so that neighbouring lanes are neighbours
         float* rec = reinterpret_cast<float*>(ws + pp.w.oRec) +
-                     (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) * kRows * (D + 2);
+                     (size_t)(2 * blockIdx.x + (first_seg ? 0 : 1)) * Ly::kRB * (D + 2);
+        const int rr = (Ly::kPair ? wg * kRows : 0) + row;
 #pragma unroll 1
         for (int c = 0; c < kHalf; c += 32) {
           float o[32];
@@ -866,16 +994,16 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(rec + ((wg * kHalf + c + i) / 4 * kRows + row) * 4) =
+            *reinterpret_cast<float4*>(rec + ((col0 + c + i) / 4 * Ly::kRB + rr) * 4) =
                 make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
-        if (wg == 0) {
-          rec[kRows * D + row] = M;
-          rec[kRows * D + kRows + row] = lsum;
+        if (Ly::kPair || wg == 0) {
+          rec[Ly::kRB * D + rr] = M;
+          rec[Ly::kRB * D + Ly::kRB + rr] = lsum;
         }
       }
       tc_fence_before();
-      mbar_arrive(o_free);
+      mbar_arrive(&o_free[Ly::kPair ? wg : 0]);
       first_seg = false;
       w = next;
     }
@@ -889,25 +1017,25 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
 }
 
 // Row blocks that span CTAs, merged in CTA order.  The grid runs over the places
-// where the list is cut, quarters of 32 rows and 32-column groups; a row block's
+// where the list is cut, groups of 32 rows and of 32 columns; a row block's
 // first cut has its merge.  lane = row; each of the eight warps takes every eighth
 // record, and the eight results are joined in order.
 constexpr int kMergeCols = 32;
 template <int D>
 __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_constant__ Params pp) {
-  constexpr int kQ = kMergeCols / 4, kGroups = D / kMergeCols;
+  constexpr int kQ = kMergeCols / 4, kGroups = D / kMergeCols, kRB = block_rows(D), kParts = kRB / 32;
   __shared__ float s_o[8][32][kMergeCols + 1];
   __shared__ float s_m[8][32], s_l[8][32];
   const BlockDecodeParams& p = pp.a;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cg = blockIdx.x % kGroups, quarter = blockIdx.x / kGroups % 4, cut = blockIdx.x / (4 * kGroups) + 1;
+  const int cg = blockIdx.x % kGroups, part = blockIdx.x / kGroups % kParts, cut = blockIdx.x / (kParts * kGroups) + 1;
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   const Head h = reinterpret_cast<const Head*>(ws + pp.w.oHead)[cut];
   if (h.rb < 0 || h.first == 0) return;
-  const int row = quarter * 32 + lane, R = p.C * p.G;
-  if (h.rb * kRows + quarter * 32 >= R) return;
+  const int row = part * 32 + lane, R = p.C * p.G;
+  if (h.rb * kRB + part * 32 >= R) return;
   const int grid = pp.w.grid, total = h.total;
   const int a = cut_at(total, grid, cut) - h.first, e = a + h.cnt;
   const int c0 = cta_of(total, grid, a), c1 = cta_of(total, grid, e - 1);
@@ -919,11 +1047,11 @@ __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_co
   for (int c = c0 + warp; c <= c1; c += 8) {
     // a CTA whose range starts inside the row block has it as its first segment
     const int slot = 2 * c + (cut_at(total, grid, c) >= a ? 0 : 1);
-    const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)slot * kRows * (D + 2);
+    const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)slot * kRB * (D + 2);
     float4 x[kQ];
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) x[i] = *reinterpret_cast<const float4*>(rec + ((cg * kQ + i) * kRows + row) * 4);
-    const float m = rec[kRows * D + row], ll = rec[kRows * D + kRows + row];
+    for (int i = 0; i < kQ; ++i) x[i] = *reinterpret_cast<const float4*>(rec + ((cg * kQ + i) * kRB + row) * 4);
+    const float m = rec[kRB * D + row], ll = rec[kRB * D + kRB + row];
     const float nm = fmaxf(M, m);
     if (nm != -INFINITY) {
       const float f = ex2(M - nm), k = ex2(m - nm);
@@ -951,7 +1079,7 @@ __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_co
   // lane = column now; four rows per warp
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int rr = warp * 4 + i, r = h.rb * kRows + quarter * 32 + rr;
+    const int rr = warp * 4 + i, r = h.rb * kRB + part * 32 + rr;
     if (r >= R) break;
     float C = -INFINITY, den = 0.f, o = 0.f;
 #pragma unroll
@@ -984,7 +1112,7 @@ cudaError_t launch(const Params& pp, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(pp.w.grid), dim3(kThreads), Lay<D>::kTotal, stream, pp);
   if (e != cudaSuccess || pp.w.grid == 1) return e;
-  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * 4 * (D / kMergeCols)), dim3(256), 0, stream, pp);
+  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * (block_rows(D) / 32) * (D / kMergeCols)), dim3(256), 0, stream, pp);
 }
 
 template <int D, bool kHiLo>

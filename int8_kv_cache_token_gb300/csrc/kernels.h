@@ -135,6 +135,19 @@ struct BlockReadParams {
   const float* k_scale;
   const float* v_scale;
 };
+// n / d for 0 <= n < 2^31 by a multiplication (the divisor's reciprocal rounded up
+// to 33 bits).
+struct FastDiv {
+  uint32_t mul, shift;
+  explicit FastDiv(uint32_t d = 1) : mul(0), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)(((((uint64_t)1 << shift) - d) << 32) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+#endif
+};
+
 constexpr int kCapDeg = 6;
 struct BlockDecodeParams {
   void* out;  // [B, Hq, D]
@@ -150,6 +163,7 @@ struct BlockDecodeParams {
   const int32_t* key_begin;  // [B] or [C], nullable: the first visible key
   const float* slopes;       // [Hq], nullable
   int B, Hq, Hkv, G, D, max_blocks, num_blocks, window;
+  FastDiv divG;     // by G
   int HG, HH;       // passes of 8 query heads per KV head; Hkv * HG
   // A chunk of one sequence (rows (token, head) of one KV head in groups of 8):
   // B = ceil(C G / 8) groups, HH = Hkv, block_tables one row, seq_lens unused.
