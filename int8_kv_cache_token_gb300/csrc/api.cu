@@ -680,7 +680,11 @@ i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, 
   p.max_blocks = max_blocks;
   p.HG = head_passes(Hq, Hkv);
   p.HH = Hkv * p.HG;
+  REQUIRE((int64_t)B * p.HH * max_blocks < (1ll << 31), I8KV_ERR_UNSUPPORTED,
+          "B=%d x %d head passes x max_blocks=%d: the block list is counted in 31 bits", B, p.HH, max_blocks);
   p.grid = i8kv::block_decode_grid(B, p.HH, max_blocks);
+  p.divHG = i8kv::FastDiv((uint32_t)p.HG);
+  p.divGrid = i8kv::FastDiv((uint32_t)p.grid);
   const size_t need = i8kv::block_decode_workspace_bytes(D, p.grid);
   REQUIRE(workspace != nullptr && workspace_bytes >= need, I8KV_ERR_WORKSPACE,
           "workspace of %zu bytes given, %zu needed", workspace_bytes, need);

@@ -52,24 +52,28 @@ struct Geo {
   static constexpr int oScale = oMerge + kBufs * kHeads * kRow * 4;  // float2 (sK, sV) per stage
   static constexpr int oBar = oScale + kWarps * kStages * 8;
   static constexpr int oStat = oBar + kWarps * kStages * 8;          // M, l [kWarps][8] each
-  static constexpr int oScan = oStat + 2 * kWarps * kHeads * 4;
-  static constexpr int kTotal = oScan + 64 * 8;
+  static constexpr int oScan = oStat + 2 * (kWarps + 1) * kHeads * 4;
+  static constexpr int kTotal = oScan + 64 * 4;
   static_assert(kTotal <= 232448, "shared memory");
 };
 
-// The workspace: a header per CTA (where its range starts), then two partial
-// records per CTA (its first and its last segment), each o [8][D], M [8], l [8].
+// The workspace: where every CTA's range starts (cuts [grid + 1] and a header
+// each), then two partial records per CTA (its first and its last segment), each
+// o [8][D], M [8], l [8].
 struct Head {
-  int b, hh;         // sequence and head pass; b = -1: an empty range
-  int first;         // visible blocks of the pair before the range
-  int nb;            // visible blocks of the pair
-  long long total;   // blocks of the flattened list
-  long long unused;
+  int b, hh;   // entry and head pass in which the range starts
+  int first;   // visible blocks of the pair before the range
+  int nb;      // visible blocks of the pair
 };
-static_assert(sizeof(Head) == 32, "16-byte aligned records");
+static_assert(sizeof(Head) == 16, "16-byte aligned records");
 __host__ __device__ constexpr int rec_floats(int D) { return kHeads * D + 2 * kHeads; }
+__host__ __device__ constexpr size_t cuts_bytes(int grid) { return (size_t)(grid + 4) / 4 * 16; }
+__device__ __forceinline__ int* cuts_of(const BlockDecodeParams& p) { return static_cast<int*>(p.ws); }
+__device__ __forceinline__ Head* heads_of(const BlockDecodeParams& p) {
+  return reinterpret_cast<Head*>(static_cast<uint8_t*>(p.ws) + cuts_bytes(p.grid));
+}
 __device__ __forceinline__ float* record(const BlockDecodeParams& p, int slot, int D) {
-  return reinterpret_cast<float*>(static_cast<uint8_t*>(p.ws) + (size_t)p.grid * sizeof(Head)) + (size_t)slot * rec_floats(D);
+  return reinterpret_cast<float*>(heads_of(p) + p.grid) + (size_t)slot * rec_floats(D);
 }
 
 // One entry of the work list: a sequence (decode), or eight (token, head) rows of
@@ -128,13 +132,13 @@ template <bool kChunk>
 __device__ __forceinline__ bool row_of(const BlockDecodeParams& p, int b, int hh, int c, int& tok, int& head) {
   if constexpr (kChunk) {
     const int r = b * kHeads + c;
-    tok = r / p.G;
-    head = hh * p.G + r % p.G;
+    tok = p.divG.div(r);
+    head = hh * p.G + r - tok * p.G;
     return r < p.C * p.G;
   } else {
-    const int in = (hh % p.HG) * kHeads + c;
+    const int kvh = p.divHG.div(hh), in = (hh - kvh * p.HG) * kHeads + c;
     tok = b;
-    head = hh / p.HG * p.G + in;
+    head = kvh * p.G + in;
     return in < p.G;
   }
 }
@@ -143,13 +147,13 @@ __device__ __forceinline__ bool row_of(const BlockDecodeParams& p, int b, int hh
 // list (sequence, head pass, block).
 struct Walk {
   int b, hh;          // current sequence and head pass
-  long long left;     // blocks of the range from here on, this segment's included
+  int left;           // blocks of the range from here on, this segment's included
   Seq s;
   int first, len;     // this segment: visible blocks [first, first + len) of the sequence
 };
 
 __device__ __forceinline__ void walk_segment(Walk& w) {
-  w.len = (int)min((long long)(w.s.nb - w.first), w.left);
+  w.len = min(w.s.nb - w.first, w.left);
 }
 // To the next segment; false at the end of the range.
 template <bool kChunk>
@@ -168,20 +172,35 @@ __device__ __forceinline__ bool walk_next(const BlockDecodeParams& p, Walk& w) {
   return true;
 }
 
-// Sum over the CTA's threads, and the sum over the threads before this one.
-template <int NW>
-__device__ __forceinline__ long long cta_scan(long long v, long long& before, long long* buf) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+// The cut of `total` blocks over `grid` CTAs: the first total % grid take one more.
+struct Cuts {
+  int per, rem;
+  __device__ __forceinline__ int at(int c) const { return per * c + min(c, rem); }
+};
+__device__ __forceinline__ Cuts cuts_for(const BlockDecodeParams& p, int total) {
+  const int per = p.divGrid.div(total);
+  return Cuts{per, total - per * p.grid};
+}
+
+// Inclusive sum over the warp's lanes.
+__device__ __forceinline__ int warp_scan(int x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
+  return x;
+}
+// Sum over the CTA's threads, and the sum over the threads before this one.
+template <int NW>
+__device__ __forceinline__ int cta_scan(int v, int& before, int* buf) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int x = warp_scan(v);
   __syncthreads();
   if (lane == 31) buf[warp] = x;
   __syncthreads();
-  long long base = 0, total = 0;
+  int base = 0, total = 0;
 #pragma unroll
   for (int i = 0; i < NW; ++i) {
     if (i < warp) base += buf[i];
@@ -189,6 +208,103 @@ __device__ __forceinline__ long long cta_scan(long long v, long long& before, lo
   }
   before = base + x - v;
   return total;
+}
+
+// A place in the list: block `first` of a pair's nb.
+struct Place {
+  int u, b, hh, first, nb;
+};
+// A cut near the border between two pairs moves there, by up to kSnap blocks and
+// half a range: the CTA would else have a segment more, whose join of the warps
+// and record cost about as much as one more round of blocks over the warps (2 us).
+template <int kSnap>
+__device__ __forceinline__ void snap(Place& at, int per) {
+  const int reach = min(kSnap, (per + 1) / 2);
+  if (at.first <= reach && at.first < at.nb) {
+    at.u -= at.first;
+    at.first = 0;
+  } else if (at.nb - at.first <= reach) {
+    at.u += at.nb - at.first;
+    at.first = at.nb;
+  }
+}
+// The CTA's range: from `from` to block `to` of the list; whether some entry has
+// no visible key.
+struct Start {
+  Place from;
+  int to;
+  bool empty;
+};
+// Up to kFew entries: each warp by itself, in one round of loads (no barrier).
+// More: the CTA's threads together.
+constexpr int kFew = 128;
+template <bool kChunk, int NW>
+__device__ __forceinline__ Start find_start(const BlockDecodeParams& p, int* buf) {
+  Start r{};
+  Place at[2];
+  const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+  int total = 0;
+  Cuts cuts;
+  if (p.B <= kFew) {
+    int nb[kFew / 32], upto[kFew / 32];
+#pragma unroll
+    for (int k = 0; k < kFew / 32; ++k) nb[k] = 32 * k + lane < p.B ? seq_of<kChunk>(p, 32 * k + lane).nb : -1;
+#pragma unroll
+    for (int k = 0; k < kFew / 32; ++k) {
+      if (32 * k >= p.B) continue;
+      r.empty |= __any_sync(0xffffffffu, nb[k] == 0);
+      upto[k] = total + warp_scan(max(nb[k], 0));
+      total = __shfl_sync(0xffffffffu, upto[k], 31);
+    }
+    total *= p.HH;
+    cuts = cuts_for(p, total);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      at[e] = Place{cuts.at(c + e), 0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < kFew / 32; ++k) {
+        if (32 * k >= p.B) continue;
+        const int s0 = (upto[k] - max(nb[k], 0)) * p.HH;
+        const uint32_t who = __ballot_sync(0xffffffffu, nb[k] > 0 && at[e].u >= s0 && at[e].u < upto[k] * p.HH);
+        if (who) {
+          const int l = __ffs(who) - 1, in = at[e].u - __shfl_sync(0xffffffffu, s0, l);
+          at[e].nb = __shfl_sync(0xffffffffu, nb[k], l);
+          at[e].b = 32 * k + l;
+          at[e].hh = in / at[e].nb;
+          at[e].first = in - at[e].hh * at[e].nb;
+        }
+      }
+    }
+  } else {
+    int before;
+    for (int b0 = 0; b0 < p.B; b0 += NW * 32)
+      total += cta_scan<NW>(b0 + tid < p.B ? seq_of<kChunk>(p, b0 + tid).nb : 0, before, buf);
+    total *= p.HH;
+    cuts = cuts_for(p, total);
+    r.empty = true;
+    Place* found = reinterpret_cast<Place*>(buf + 32);
+    if (tid < 2) found[tid] = Place{cuts.at(c + tid), 0, 0, 0, 0};
+    int run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += NW * 32) {
+      const int nb = b0 + tid < p.B ? seq_of<kChunk>(p, b0 + tid).nb : 0;
+      const int here = cta_scan<NW>(nb, before, buf);
+      const int s0 = (run + before) * p.HH;
+      for (int e = 0; e < 2; ++e) {
+        const int u = cuts.at(c + e);
+        if (u >= s0 && u < s0 + nb * p.HH) found[e] = Place{u, b0 + tid, (u - s0) / nb, (u - s0) % nb, nb};
+      }
+      run += here;
+    }
+    __syncthreads();
+    at[0] = found[0];
+    at[1] = found[1];
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (at[e].u > 0 && at[e].u < total) snap<NW>(at[e], cuts.per);
+  r.from = at[0];
+  r.to = at[1].u;
+  return r;
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -225,7 +341,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Gm::oBar) + warp * NS;
   float* statM = reinterpret_cast<float*>(smem + Gm::oStat);
   float* statL = statM + NW * kHeads;
-  long long* scan = reinterpret_cast<long long*>(smem + Gm::oScan);
+  float* joint = statL + NW * kHeads;  // M, l of the segment
+  int* scan = reinterpret_cast<int*>(smem + Gm::oScan);
 
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&bar[i], 1);
@@ -236,53 +353,45 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   griddep_launch_dependents();
 
   // ---- this CTA's range of the flattened list, and where it starts ----
-  long long total = 0, mine;
-  for (int b0 = 0; b0 < p.B; b0 += Gm::kThreads) {
-    const int b = b0 + tid;
-    const int nb = b < p.B ? seq_of<kChunk>(p, b).nb : 0;
-    if (!kChunk && b < p.B && blockIdx.x == 0 && p.seq_lens[b] > p.max_blocks * kBS) record_error(2);
-    total += cta_scan<NW>(nb, mine, scan);
-  }
-  total *= p.HH;
-  const long long u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
-  // entries without a visible key: zero rows
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
-    if (seq_of<kChunk>(p, b).nb == 0)
-      for (int i = tid; i < p.HH * kHeads * (D / 4); i += Gm::kThreads) {
-        const int c4 = (i % (D / 4)) * 4, c = i / (D / 4);
-        int tok, hd;
-        if (row_of<kChunk>(p, b, c / kHeads, c % kHeads, tok, hd))
-          store_out4(p.out, p.out_bf16, ((size_t)tok * p.Hq + hd) * D + c4, make_float4(0.f, 0.f, 0.f, 0.f));
-      }
-  Head* head = static_cast<Head*>(p.ws) + blockIdx.x;
-  if (u0 >= u1) {
-    if (tid == 0) head->b = -1;
-    return;
-  }
-  int* start = reinterpret_cast<int*>(scan + 32);  // sequence, head pass, block
-  if (tid < 3) start[tid] = 0;
-  long long run = 0;
-  for (int b0 = 0; b0 < p.B; b0 += Gm::kThreads) {
-    const int b = b0 + tid;
-    const int nb = b < p.B ? seq_of<kChunk>(p, b).nb : 0;
-    const long long sum = cta_scan<NW>(nb, mine, scan);
-    const long long s0 = (run + mine) * p.HH;
-    if (u0 >= s0 && u0 < s0 + (long long)nb * p.HH) {
-      start[0] = b;
-      start[1] = (int)((u0 - s0) / nb);
-      start[2] = (int)((u0 - s0) % nb);
-    }
-    run += sum;
-  }
-  __syncthreads();
+  const Start at = find_start<kChunk, NW>(p, scan);
+  if (!kChunk && blockIdx.x == 0)
+    for (int b = tid; b < p.B; b += Gm::kThreads)
+      if (p.seq_lens[b] > p.max_blocks * kBS) record_error(2);
+  if (at.empty)  // entries without a visible key: zero rows
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+      if (seq_of<kChunk>(p, b).nb == 0)
+        for (int i = tid; i < p.HH * kHeads * (D / 4); i += Gm::kThreads) {
+          const int c4 = (i % (D / 4)) * 4, c = i / (D / 4);
+          int tok, hd;
+          if (row_of<kChunk>(p, b, c / kHeads, c % kHeads, tok, hd))
+            store_out4(p.out, p.out_bf16, ((size_t)tok * p.Hq + hd) * D + c4, make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+  if (tid == 0) cuts_of(p)[blockIdx.x] = at.from.u;
+  if (tid == 0 && blockIdx.x + 1 == gridDim.x) cuts_of(p)[gridDim.x] = at.to;
+  if (at.from.u >= at.to) return;
   Walk w;
-  w.b = start[0];
-  w.hh = start[1];
-  w.first = start[2];
-  w.left = u1 - u0;
+  w.b = at.from.b;
+  w.hh = at.from.hh;
+  w.first = at.from.first;
+  w.left = at.to - at.from.u;
+  w.len = 0;
   w.s = seq_of<kChunk>(p, w.b);
   walk_segment(w);
-  if (tid == 0) *head = Head{w.b, w.hh, w.first, w.s.nb, total, 0};
+  if (w.len == 0 && !walk_next<kChunk>(p, w)) return;  // the range starts with the next pair
+  if (tid == 0) heads_of(p)[blockIdx.x] = Head{w.b, w.hh, w.first, w.s.nb};
+
+  // The query rows of a segment as they are: row g, dims 16 i + 4 t4 .. + 3.
+  uint2 raw[D / 16];
+  auto load_q = [&](const Walk& x) {
+    int tok, hd;
+    const bool in = row_of<kChunk>(p, x.b, x.hh, g, tok, hd);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      raw[i] = make_uint2(0, 0);
+      if (in) raw[i] = __ldg(reinterpret_cast<const uint2*>(p.q + (int64_t)tok * p.q_stride + (size_t)hd * D + 16 * i + 4 * t4));
+    }
+  };
+  load_q(w);
 
   // ---- the page copies: a walk of their own, NS blocks ahead of the consumer ----
   Walk c = w;
@@ -314,7 +423,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
       }
     }
     const int phys = __shfl_sync(0xffffffffu, table, k - table_at);
-    const int kvh = kChunk ? c.hh : c.hh / p.HG;
+    const int kvh = kChunk ? c.hh : p.divHG.div(c.hh);
     const int slot = c_n % NS;
     const size_t ph = (size_t)phys * p.Hkv + kvh;
     if (lane == 0) mbar_expect_tx(&bar[slot], Gm::kStage);
@@ -352,10 +461,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   bool first_seg = true;
   for (;;) {
     // ---- a segment: blocks [first, first + len) of sequence b for one head pass ----
-    // the rows of this lane: row g as a row of q, rows 2 t4 and 2 t4 + 1 as columns
-    // of the scores and the output
-    int q_tok, q_head;
-    const bool q_row = row_of<kChunk>(p, w.b, w.hh, g, q_tok, q_head);
+    // rows 2 t4 and 2 t4 + 1 are this lane's columns of the scores and the output
     int lo0 = w.s.lo, hi0 = w.s.hi, lo1 = w.s.lo, hi1 = w.s.hi, pos0 = w.s.hi - 1, pos1 = w.s.hi - 1;
     float sl0 = 0.f, sl1 = 0.f;
     {
@@ -380,14 +486,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
     uint32_t qf[D / 16][2];
     float qs;
     {
-      uint2 raw[D / 16];
       float am = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        raw[i] = make_uint2(0, 0);
-        if (q_row)
-          raw[i] = __ldg(reinterpret_cast<const uint2*>(p.q + (int64_t)q_tok * p.q_stride + (size_t)q_head * D + 16 * i + 4 * t4));
-      }
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         am = fmaxf(am, fmaxf(fabsf(__uint_as_float(raw[i].x << 16)), fabsf(__uint_as_float(raw[i].x & 0xffff0000u))));
@@ -550,16 +649,35 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
       C1 = fmaxf(C1, statM[i * kHeads + 2 * t4 + 1]);
     }
     const float f0 = M0 == -INFINITY ? 0.f : ex2(M0 - C0), f1 = M1 == -INFINITY ? 0.f : ex2(M1 - C1);
-    float* buf = merge + (warp % Gm::kBufs) * (kHeads * Gm::kRow);
+    // Each head's maximum and sum, once, by eight lanes of the last warp.
+    if (warp == NW - 1 && lane < kHeads) {
+      float C = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) C = fmaxf(C, statM[k * kHeads + lane]);
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        const float m = statM[k * kHeads + lane];
+        if (m != -INFINITY) l = __fmaf_rn(statL[k * kHeads + lane], ex2(m - C), l);
+      }
+      joint[lane] = C;
+      joint[kHeads + lane] = l;
+    }
+    // The CTA's last segment has the page ring to itself: a buffer per warp, one
+    // round.  Before that the next segment's pages are on their way into the ring,
+    // and four warps at a time add to four buffers.
+    const bool end = w.left == w.len;
+    const int bufs = end ? NW : Gm::kBufs, rounds = NW / bufs;
+    float* joined = end ? reinterpret_cast<float*>(smem + Gm::oRing) : merge;
+    float* buf = joined + (warp % bufs) * (kHeads * Gm::kRow);
 #pragma unroll 1
-    for (int r = NW / Gm::kBufs - 1; r >= 0; --r) {  // four warps at a time, the last ones first
-      if (warp / Gm::kBufs == r) {
+    for (int r = rounds - 1; r >= 0; --r) {  // the last warps first
+      if (warp / bufs == r) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float& x = buf[(2 * t4 + (j & 1)) * Gm::kRow + 16 * k + g + (j >> 1) * 8];
-            x = __fmaf_rn(o[k][j], (j & 1) ? f1 : f0, r == NW / Gm::kBufs - 1 ? 0.f : x);
+            x = __fmaf_rn(o[k][j], (j & 1) ? f1 : f0, r == rounds - 1 ? 0.f : x);
           }
       }
       __syncthreads();
@@ -570,23 +688,16 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
       const int h = i / (D / 4), c4 = (i % (D / 4)) * 4;
       int tok, hd;
       if (!row_of<kChunk>(p, w.b, w.hh, h, tok, hd)) continue;
-      float4 acc = *reinterpret_cast<const float4*>(merge + h * Gm::kRow + c4);
-#pragma unroll
-      for (int k = 1; k < Gm::kBufs; ++k) {
-        const float4 x = *reinterpret_cast<const float4*>(merge + (k * kHeads + h) * Gm::kRow + c4);
+      float4 acc = *reinterpret_cast<const float4*>(joined + h * Gm::kRow + c4);
+#pragma unroll 4
+      for (int k = 1; k < bufs; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(joined + (k * kHeads + h) * Gm::kRow + c4);
         acc.x += x.x;
         acc.y += x.y;
         acc.z += x.z;
         acc.w += x.w;
       }
-      float C = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int k = 0; k < NW; ++k) C = fmaxf(C, statM[k * kHeads + h]);
-#pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        const float m = statM[k * kHeads + h];
-        if (m != -INFINITY) l = __fmaf_rn(statL[k * kHeads + h], ex2(m - C), l);
-      }
+      const float C = joint[h], l = joint[kHeads + h];
       if (whole) {
         const float iv = l > 0.f ? 1.0f / l : 0.f;  // a row without a visible key is zero
         store_out4(p.out, p.out_bf16, ((size_t)tok * p.Hq + hd) * D + c4,
@@ -601,6 +712,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
     }
     first_seg = false;
     if (!walk_next<kChunk>(p, w)) break;
+    load_q(w);
     __syncthreads();  // the merge buffers are free again
   }
   // after a time-out: the copies still under way get one more (bounded) wait
@@ -609,49 +721,62 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
 }
 
 // The records of the pairs that span CTAs, merged in CTA order.  A pair is cut
-// only where a CTA's range starts, so the grid runs over those places (c0 + 1 ..)
-// and heads; the first cut inside a pair has its merge.  D / 4 columns of threads
-// in kParts parts, each part every kParts-th record.
-constexpr int kMergeThreads = 256;
+// only where a CTA's range starts, so the grid runs over those places and rows;
+// the first cut inside a pair has its merge.  D / 4 columns of threads in kParts
+// parts, each part every kParts-th record, six records in flight.
+constexpr int kParts = 8;
 
 template <int D, bool kChunk>
-__global__ void __launch_bounds__(kMergeThreads) block_decode_merge_kernel(BlockDecodeParams p, int heads) {
-  constexpr int kCols = D / 4, kParts = kMergeThreads / kCols;
+__global__ void __launch_bounds__(D / 4 * kParts) block_decode_merge_kernel(BlockDecodeParams p, int rows) {
+  constexpr int kCols = D / 4, kThreads = kCols * kParts;
   __shared__ float4 s_o[kParts][kCols];
   __shared__ float s_ml[kParts][2];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
-  const int h = blockIdx.x % heads, cut = blockIdx.x / heads + 1;
-  const Head hd = static_cast<const Head*>(p.ws)[cut];
-  if (hd.b < 0 || hd.first == 0) return;  // an empty range, or no pair is cut here
+  const int tid = threadIdx.x, grid = p.grid;
+  const int h = blockIdx.x % rows, cut = blockIdx.x / rows + 1;
+  const int* cuts = cuts_of(p);
+  const int here = cuts[cut], prev = cuts[cut - 1], next = cuts[cut + 1];
+  const Head hd = heads_of(p)[cut];
+  const int later = cut + 1 + tid < grid ? cuts[cut + 1 + tid] : 0x7fffffff;
+  if (here >= next || hd.first == 0) return;  // an empty range, or no pair is cut here
+  const int a = here - hd.first, e = a + hd.nb;  // the pair's blocks of the list
+  if (prev > a) return;  // not the first cut of the pair
   int tok, qh;
   if (!row_of<kChunk>(p, hd.b, hd.hh, h, tok, qh)) return;
-  const size_t orow = ((size_t)tok * p.Hq + qh) * D;
-  const long long total = hd.total, grid = p.grid;
-  auto begin_of = [&](long long c) { return total * c / grid; };
-  auto cta_of = [&](long long u) { return (int)(((u + 1) * grid - 1) / total); };
-  // the pair's blocks [a, e) of the flattened list lie in the ranges of CTAs c0 .. c1
-  const long long a = begin_of(cut) - hd.first, e = a + hd.nb;
-  const int c0 = cta_of(a), c1 = cta_of(e - 1);
-  if (cut != cta_of(begin_of(c0 + 1))) return;  // not the first cut of the pair
+  // CTA c0 has the pair's beginning (cuts inside a pair differ, so it is the one
+  // before); c1 is the last whose range starts before the pair's end
+  const int c0 = cut - 1;
+  int c1 = cut + __syncthreads_count(later < e);
+  for (int c = cut + 1 + kThreads; c < grid; c += kThreads) c1 += __syncthreads_count(c + tid < grid && cuts[c + tid] < e);
   const int col = tid % kCols, part = tid / kCols;
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0 + part; c <= c1; c += kParts) {
-    if (begin_of(c) == begin_of(c + 1)) continue;  // an empty range (fewer blocks than CTAs)
-    // a CTA whose range starts inside the pair has it as its first segment
-    const float* rec = record(p, 2 * c + (begin_of(c) >= a ? 0 : 1), D);
-    const float4 x = *reinterpret_cast<const float4*>(rec + h * D + 4 * col);
-    const float m = rec[kHeads * D + h], ll = rec[kHeads * D + kHeads + h];
-    const float nm = fmaxf(M, m);
-    if (nm != -INFINITY) {
-      const float f = ex2(M - nm), k = ex2(m - nm);  // 2^-inf = 0
-      acc.x = acc.x * f + x.x * k;
-      acc.y = acc.y * f + x.y * k;
-      acc.z = acc.z * f + x.z * k;
-      acc.w = acc.w * f + x.w * k;
-      l = l * f + ll * k;
+  for (int c = c0 + part; c <= c1; c += 6 * kParts) {
+    float4 x[6];
+    float m[6], ll[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      const int cc = c + k * kParts;
+      m[k] = -INFINITY;
+      if (cc <= c1) {
+        // a CTA whose range starts inside the pair has it as its first segment
+        const float* rec = record(p, 2 * cc + (cc > c0 || prev == a ? 0 : 1), D);
+        x[k] = *reinterpret_cast<const float4*>(rec + h * D + 4 * col);
+        m[k] = rec[kHeads * D + h];
+        ll[k] = rec[kHeads * D + kHeads + h];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      const float nm = fmaxf(M, m[k]);
+      if (m[k] == -INFINITY) continue;
+      const float f = ex2(M - nm), g = ex2(m[k] - nm);  // 2^-inf = 0
+      acc.x = acc.x * f + x[k].x * g;
+      acc.y = acc.y * f + x[k].y * g;
+      acc.z = acc.z * f + x[k].z * g;
+      acc.w = acc.w * f + x[k].w * g;
+      l = l * f + ll[k] * g;
       M = nm;
     }
   }
@@ -679,7 +804,7 @@ __global__ void __launch_bounds__(kMergeThreads) block_decode_merge_kernel(Block
       den += s_ml[k][1] * f;
     }
     const float iv = den > 0.f ? 1.0f / den : 0.f;
-    store_out4(p.out, p.out_bf16, orow + 4 * col, make_float4(r.x * iv, r.y * iv, r.z * iv, r.w * iv));
+    store_out4(p.out, p.out_bf16, ((size_t)tok * p.Hq + qh) * D + 4 * col, make_float4(r.x * iv, r.y * iv, r.z * iv, r.w * iv));
   }
 }
 
@@ -698,9 +823,8 @@ cudaError_t launch_d(const BlockDecodeParams& p, cudaStream_t stream) {
   const cudaError_t e = launch_pdl(kernel, dim3(p.grid), dim3(Geo<D>::kThreads), Geo<D>::kTotal, stream, p);
   if (e != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
-  const int heads = !kChunk && p.G < kHeads ? p.G : kHeads;
-  return launch_pdl(block_decode_merge_kernel<D, kChunk>, dim3((p.grid - 1) * heads), dim3(kMergeThreads), 0, stream, p,
-                    heads);
+  const int rows = !kChunk && p.G < kHeads ? p.G : kHeads;
+  return launch_pdl(block_decode_merge_kernel<D, kChunk>, dim3((p.grid - 1) * rows), dim3(D / 4 * kParts), 0, stream, p, rows);
 }
 
 template <int D, bool kChunk>
@@ -710,24 +834,28 @@ cudaError_t launch_v(const BlockDecodeParams& p, cudaStream_t stream) {
   return cap ? launch_d<D, kChunk, true, true>(p, stream) : launch_d<D, kChunk, false, true>(p, stream);
 }
 
-int device_sms() {
+}  // namespace
+
+// The SMs of the current device, asked once per device.
+int block_device_sms() {
+  static int known[64] = {0};
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
+  if (dev >= 0 && dev < 64 && known[dev] > 0) return known[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 1;
+  if (dev >= 0 && dev < 64) known[dev] = n;
   return n;
 }
-
-}  // namespace
 
 // CTAs of the attention kernel: one per SM, or one per block where there are fewer.
 int block_decode_grid(int entries, int HH, int max_blocks) {
   const long long most = (long long)entries * HH * max_blocks;
-  const int sms = device_sms();
+  const int sms = block_device_sms();
   return most < sms ? (int)(most > 0 ? most : 1) : sms;
 }
 
 size_t block_decode_workspace_bytes(int D, int grid) {
-  return (size_t)grid * (sizeof(Head) + 2 * rec_floats(D) * sizeof(float));
+  return cuts_bytes(grid) + (size_t)grid * (sizeof(Head) + 2 * rec_floats(D) * sizeof(float));
 }
 
 cudaError_t launch_block_decode(const BlockDecodeParams& p, cudaStream_t stream) {

@@ -13,16 +13,9 @@ namespace {
 // eight rows, each reading the int8 cache itself.
 constexpr int kFewRows = 64;
 
-int device_sms() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
-  return n;
-}
-
 int grid_of(const bp::Plan& w, int Hkv) {
   const int64_t most = (int64_t)w.nrb * w.ntiles * Hkv;
-  const int sms = device_sms();
+  const int sms = block_device_sms();
   return most < sms ? (int)most : sms;
 }
 
@@ -33,7 +26,7 @@ size_t block_prefix_workspace_bytes(int H, int C, int G, int Hkv, int D) {
   if (rows <= kFewRows)
     return block_decode_workspace_bytes(D, block_decode_grid((int)((rows + 7) / 8), Hkv, (H + C + 15) / 16));
   // without a window: the largest plan
-  return bp::plan_of(H, C, G, Hkv, D, 0, device_sms()).bytes;
+  return bp::plan_of(H, C, G, Hkv, D, 0, block_device_sms()).bytes;
 }
 
 cudaError_t launch_block_prefix(BlockDecodeParams p, cudaStream_t stream) {
@@ -44,6 +37,7 @@ cudaError_t launch_block_prefix(BlockDecodeParams p, cudaStream_t stream) {
     p.HH = p.Hkv;
     p.max_blocks = (p.H + p.C + 15) / 16;
     p.grid = block_decode_grid(p.B, p.HH, p.max_blocks);
+    p.divGrid = FastDiv((uint32_t)p.grid);
     return launch_block_chunk_rows(p, stream);
   }
   bp::Params pp{p, bp::plan_of(p.H, p.C, p.G, p.Hkv, p.D, p.window, 1)};

@@ -829,16 +829,15 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
             for (int i = 0; i < kKeys; ++i) v[i] = __fmaf_rn(2.f * slope, fmaxf(d0 + (float)i, 0.f), v[i]);
           }
         }
-        // hidden keys
-        if (__any_sync(0xffffffffu, key0 + kKeys > hi)) {
-          const int e = hi - key0;
+        // hidden keys: only blocks of 16 in which some row of the warp has any
+        if (!__all_sync(0xffffffffu, key0 >= lo && key0 + kKeys <= hi)) {
+          const int a = lo - key0, e = hi - key0;
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) v[i] = i < e ? v[i] : -INFINITY;
-        }
-        if (__any_sync(0xffffffffu, key0 < lo)) {
-          const int a = lo - key0;
+          for (int b = 0; b < kBlk; ++b)
+            if (__any_sync(0xffffffffu, a > b * kBS || e < (b + 1) * kBS)) {
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) v[i] = i >= a ? v[i] : -INFINITY;
+              for (int i = b * kBS; i < (b + 1) * kBS; ++i) v[i] = i >= a && i < e ? v[i] : -INFINITY;
+            }
         }
         float mb[8];
 #pragma unroll

@@ -163,7 +163,7 @@ struct BlockDecodeParams {
   const int32_t* key_begin;  // [B] or [C], nullable: the first visible key
   const float* slopes;       // [Hq], nullable
   int B, Hq, Hkv, G, D, max_blocks, num_blocks, window;
-  FastDiv divG;     // by G
+  FastDiv divG, divHG, divGrid;  // by G, HG and grid
   int HG, HH;       // passes of 8 query heads per KV head; Hkv * HG
   // A chunk of one sequence (rows (token, head) of one KV head in groups of 8):
   // B = ceil(C G / 8) groups, HH = Hkv, block_tables one row, seq_lens unused.
@@ -210,6 +210,7 @@ cudaError_t launch_debug_prefix(const PrefixParams& p, cudaStream_t stream);
 
 cudaError_t launch_block_kv_write(const BlockRaggedParams& r, const BlockWriteParams& p, cudaStream_t stream);
 cudaError_t launch_block_kv_read(const BlockRaggedParams& r, const BlockReadParams& p, cudaStream_t stream);
+int block_device_sms();
 int block_decode_grid(int entries, int HH, int max_blocks);
 size_t block_decode_workspace_bytes(int D, int grid);
 cudaError_t launch_block_decode(const BlockDecodeParams& p, cudaStream_t stream);
