@@ -9,6 +9,7 @@ the library is not built, or a call fails, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -445,21 +446,26 @@ def _require(cond: bool, msg: str):
         raise I8KVError(ERR_INVALID_ARG, msg)
 
 
-def _at(t, dtype, shape, dev, name) -> int | None:
-    """Device address of a contiguous tensor of exactly this dtype, shape and device (None stays None)."""
+# The calls below are short, and a decode step makes many of them: the checks are
+# a few attribute reads per tensor, with the message built only on a refusal.
+_i8, _i32, _f32, _bf16_t = torch.int8, torch.int32, torch.float32, torch.bfloat16
+
+
+def _at(t, dtype, shape, dev: int, name) -> int | None:
+    """Device address of a contiguous tensor of exactly this dtype, shape and device index (None stays None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise I8KVError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, "
-                                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
-                                         f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise I8KVError(ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, "
+                                     f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-def _rows(t, shape, dev, name):
+def _rows(t, shape, dev: int, name):
     """(address, row stride in elements) of bf16 rows [N, H, D]: each row contiguous, the rows any stride apart."""
-    if t.dtype is not torch.bfloat16 or t.device != dev or t.shape != shape:
-        raise I8KVError(ERR_INVALID_ARG, f"{name} must be a torch.bfloat16 tensor of shape {tuple(shape)} on {dev}, "
+    if t.dtype is not _bf16_t or t.shape != shape or t.get_device() != dev:
+        raise I8KVError(ERR_INVALID_ARG, f"{name} must be a torch.bfloat16 tensor of shape {tuple(shape)} on cuda:{dev}, "
                                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     n, h, d = shape
     if t.is_contiguous():
@@ -470,36 +476,36 @@ def _rows(t, shape, dev, name):
 
 
 def _block_geom(k_cache, v_cache, k_scale, v_scale):
-    """(addresses, NB, Hkv, D, device) of a block-scaled cache."""
+    """(addresses, NB, Hkv, D, device index) of a block-scaled cache."""
     NB, Hkv, D = _cache_geom(k_cache, 16)
-    dev = k_cache.device
-    _require(dev.type == "cuda", "k_cache must be a CUDA tensor")
-    return (_at(k_cache, torch.int8, k_cache.shape, dev, "k_cache"),
-            _at(v_cache, torch.int8, (NB, Hkv, D, BLOCK_SIZE), dev, "v_cache"),
-            _at(k_scale, torch.float32, (NB, Hkv), dev, "k_scale"),
-            _at(v_scale, torch.float32, (NB, Hkv), dev, "v_scale")), NB, Hkv, D, dev
+    dev = k_cache.get_device()
+    _require(dev >= 0, "k_cache must be a CUDA tensor")
+    return (_at(k_cache, _i8, k_cache.shape, dev, "k_cache"), _at(v_cache, _i8, (NB, Hkv, D, BLOCK_SIZE), dev, "v_cache"),
+            _at(k_scale, _f32, (NB, Hkv), dev, "k_scale"), _at(v_scale, _f32, (NB, Hkv), dev, "v_scale")), NB, Hkv, D, dev
 
 
-def _call(fn, dev, stream, *args):
+def _call(fn, dev: int, stream, *args):
     """Run a C entry point on `stream` (the device's current one when None) with the tensors' device current."""
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(dev)
     else:
-        _require(stream.device == dev, f"stream is on {stream.device}, the tensors on {dev}")
+        _require(stream.device.index == dev, f"stream is on {stream.device}, the tensors on cuda:{dev}")
         handle = stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, handle))
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, handle))
+            status = fn(*args, handle)
+    if status != OK:
+        _check(status)
 
 
 def _ragged(seq_lens, block_tables, cu_tokens, T, dev):
     _require(block_tables.dim() == 2, "block_tables must be [B, max_blocks]")
     B, mb = block_tables.shape
     _require(cu_tokens is not None or T == B, f"{T} rows for {B} sequences need cu_tokens")
-    return (_at(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), _at(seq_lens, torch.int32, (B,), dev, "seq_lens"),
-            _at(block_tables, torch.int32, (B, mb), dev, "block_tables"), B, mb)
+    return (_at(cu_tokens, _i32, (B + 1,), dev, "cu_tokens"), _at(seq_lens, _i32, (B,), dev, "seq_lens"),
+            _at(block_tables, _i32, block_tables.shape, dev, "block_tables"), B, mb)
 
 
 def block_kv_write(k, v, seq_lens, block_tables, k_cache, v_cache, k_scale, v_scale, cu_tokens=None, stream=None):
@@ -529,35 +535,45 @@ def block_kv_read(k_out, v_out, seq_lens, block_tables, k_cache, v_cache, k_scal
 
 
 def _out_code(t) -> int:
-    _require(t.dtype in (torch.float32, torch.bfloat16), f"out must be float32 or bfloat16, got {t.dtype}")
-    return OUT_F32 if t.dtype is torch.float32 else OUT_BF16
+    if t.dtype is _bf16_t:
+        return OUT_BF16
+    _require(t.dtype is _f32, f"out must be float32 or bfloat16, got {t.dtype}")
+    return OUT_F32
 
 
-def _workspace(workspace, need: int, dev, stream):
-    """(address, bytes) of the given workspace, or of one allocated for this call on its stream."""
+@functools.lru_cache(maxsize=None)
+def _cuda(dev: int) -> torch.device:
+    return torch.device("cuda", dev)  # an int as `device` costs several us a call
+
+
+@functools.lru_cache(maxsize=1024)
+def _block_bytes(name: str, dev: int, *shape) -> int:
+    """A workspace size: it depends on the shape and the device's number of SMs alone."""
+    with torch.cuda.device(dev):
+        return max(int(getattr(lib(), name)(*shape)), 16)
+
+
+def _workspace(workspace, dev: int, stream, name: str, *shape):
+    """(tensor, bytes): the given workspace, or one allocated for this call on its stream."""
     if workspace is None:
+        n = _block_bytes(name, dev, *shape)
         if stream is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _require(workspace.device == dev and workspace.is_contiguous(), f"workspace must be contiguous on {dev}")
+            return torch.empty(n, dtype=torch.uint8, device=_cuda(dev)), n
+        with torch.cuda.stream(stream):
+            return torch.empty(n, dtype=torch.uint8, device=_cuda(dev)), n
+    _require(workspace.get_device() == dev and workspace.is_contiguous(), f"workspace must be contiguous on cuda:{dev}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _device_bytes(fn, dev, *args) -> int:
-    """A workspace size (it depends on the device's number of SMs)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return int(fn(*args))
-    with torch.cuda.device(dev):
-        return int(fn(*args))
+def _device_index(device) -> int:
+    dev = torch.device(device)
+    _require(dev.type == "cuda", f"a workspace lives on a CUDA device, not on {dev}")
+    return torch.cuda.current_device() if dev.index is None else dev.index
 
 
 def block_decode_workspace(B: int, Hq: int, Hkv: int, D: int, max_blocks: int, device="cuda") -> torch.Tensor:
     """A block_decode_attn workspace (reusable by later calls on the same stream)."""
-    dev = torch.device(device)
-    n = _device_bytes(lib().i8kv_block_decode_workspace_bytes, dev, B, Hq, Hkv, D, max_blocks)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    return _workspace(None, _device_index(device), None, "i8kv_block_decode_workspace_bytes", B, Hq, Hkv, D, max_blocks)[0]
 
 
 def block_decode_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, workspace=None,
@@ -571,26 +587,23 @@ def block_decode_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, 
     on.  workspace: a block_decode_workspace(...) tensor; when None one is allocated for this call."""
     cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
     _require(q.dim() == 3, "q must be [B, Hq, D]")
-    B, Hq = q.shape[0], q.shape[1]
-    qp, qs = _rows(q, (B, Hq, D), dev, "q")
-    op = _at(out, out.dtype, (B, Hq, D), dev, "out")
+    B, Hq, _ = shape = q.shape
+    _require(shape[2] == D, f"q has head_dim {shape[2]}, the cache {D}")
+    qp, qs = _rows(q, shape, dev, "q")
     code = _out_code(out)
-    _, sl, bt, Bt, mb = _ragged(seq_lens, block_tables, None, B, dev)
-    kb = _at(key_begin, torch.int32, (B,), dev, "key_begin")
-    al = _at(alibi_slopes, torch.float32, (Hq,), dev, "alibi_slopes")
-    need = 0
-    if workspace is None:
-        need = _device_bytes(lib().i8kv_block_decode_workspace_bytes, dev, B, Hq, Hkv, D, mb)
-    ws, n = _workspace(workspace, need, dev, stream)
+    op = _at(out, out.dtype, shape, dev, "out")
+    _, sl, bt, _, mb = _ragged(seq_lens, block_tables, None, B, dev)
+    kb = _at(key_begin, _i32, (B,), dev, "key_begin")
+    al = _at(alibi_slopes, _f32, (Hq,), dev, "alibi_slopes")
+    ws, n = _workspace(workspace, dev, stream, "i8kv_block_decode_workspace_bytes", B, Hq, Hkv, D, mb)
     _call(lib().i8kv_block_decode_attn, dev, stream, op, code, qp, qs, *cache, bt, sl, kb, al, B, Hq, Hkv, D, BLOCK_SIZE,
           mb, NB, softmax_scale, softcap, window, ws.data_ptr(), n)
 
 
 def block_prefix_workspace(history_len: int, chunk_len: int, Hq: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
     """A block_prefix_attn workspace (reusable by later calls on the same stream)."""
-    dev = torch.device(device)
-    n = _device_bytes(lib().i8kv_block_prefix_workspace_bytes, dev, history_len, chunk_len, Hq, Hkv, D)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=dev)
+    return _workspace(None, _device_index(device), None, "i8kv_block_prefix_workspace_bytes", int(history_len), chunk_len, Hq,
+                      Hkv, D)[0]
 
 
 def block_prefix_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_table, history_len: int, workspace=None,
@@ -603,20 +616,18 @@ def block_prefix_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_table, h
     without key_end).  softcap, alibi_slopes and workspace as in block_decode_attn."""
     cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
     _require(q.dim() == 3, "q must be [C, Hq, D]")
-    C, Hq = q.shape[0], q.shape[1]
-    qp, qs = _rows(q, (C, Hq, D), dev, "q")
-    op = _at(out, out.dtype, (C, Hq, D), dev, "out")
+    C, Hq, _ = shape = q.shape
+    _require(shape[2] == D, f"q has head_dim {shape[2]}, the cache {D}")
+    qp, qs = _rows(q, shape, dev, "q")
     code = _out_code(out)
+    op = _at(out, out.dtype, shape, dev, "out")
     history_len = int(history_len)
     _require(block_table.dim() == 1 and block_table.shape[0] * BLOCK_SIZE >= history_len + C,
              f"block_table must be 1-D and cover {history_len + C} positions")
-    bt = _at(block_table, torch.int32, block_table.shape, dev, "block_table")
-    kb = _at(key_begin, torch.int32, (C,), dev, "key_begin")
-    ke = _at(key_end, torch.int32, (C,), dev, "key_end")
-    al = _at(alibi_slopes, torch.float32, (Hq,), dev, "alibi_slopes")
-    need = 0
-    if workspace is None:
-        need = _device_bytes(lib().i8kv_block_prefix_workspace_bytes, dev, history_len, C, Hq, Hkv, D)
-    ws, n = _workspace(workspace, need, dev, stream)
+    bt = _at(block_table, _i32, block_table.shape, dev, "block_table")
+    kb = _at(key_begin, _i32, (C,), dev, "key_begin")
+    ke = _at(key_end, _i32, (C,), dev, "key_end")
+    al = _at(alibi_slopes, _f32, (Hq,), dev, "alibi_slopes")
+    ws, n = _workspace(workspace, dev, stream, "i8kv_block_prefix_workspace_bytes", history_len, C, Hq, Hkv, D)
     _call(lib().i8kv_block_prefix_attn, dev, stream, op, code, qp, qs, *cache, bt, history_len, C, kb, ke, al, Hq, Hkv, D,
           BLOCK_SIZE, NB, softmax_scale, softcap, window, ws.data_ptr(), n)

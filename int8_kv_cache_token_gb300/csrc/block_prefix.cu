@@ -43,6 +43,7 @@ cudaError_t launch_block_prefix(BlockDecodeParams p, cudaStream_t stream) {
   bp::Params pp{p, bp::plan_of(p.H, p.C, p.G, p.Hkv, p.D, p.window, 1)};
   const int grid = grid_of(pp.w, p.Hkv);
   pp.w = bp::plan_of(p.H, p.C, p.G, p.Hkv, p.D, p.window, grid);
+  pp.a.divGrid = FastDiv((uint32_t)grid);
   if (p.D == 256) return launch_block_prefix_256(pp, stream);
   if (p.D == 128) return launch_block_prefix_128(pp, stream);
   return launch_block_prefix_64(pp, stream);

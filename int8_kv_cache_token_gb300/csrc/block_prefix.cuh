@@ -64,7 +64,7 @@ constexpr int kScales = 3 * kBlk;  // per tile: sK, log2 sV, 1 / sV of its block
 // The workspace (all offsets multiples of 128 bytes).
 struct Head {
   int rb, kvh, first, cnt;  // where a CTA's range starts: row block (-1: empty range), KV head, tile, tiles
-  int total, pad[3];
+  int per, rem, pad[2];     // the cut of the list (cut_at)
 };
 static_assert(sizeof(Head) == 32, "");
 struct Range {
@@ -138,8 +138,8 @@ __device__ __forceinline__ uint32_t bf16x2_codes(uint32_t w, int i) {
   return bf16x2_rn((float)(int8_t)((w >> (8 * i)) & 0xffu), (float)(int8_t)((w >> (8 * i + 8)) & 0xffu));
 }
 
-// ---- operand tiles and scales: one CTA per (tile, KV head); also the row blocks'
-// tile ranges, spread over the CTAs' warps.
+// ---- operand tiles and scales: one CTA per (tile, KV head) for the keys and one
+// for the values; also the row blocks' tile ranges, spread over the latter's warps.
 template <int D>
 __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant__ Params pp) {
   const BlockDecodeParams& p = pp.a;
@@ -147,11 +147,12 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile = blockIdx.x, kvh = blockIdx.y;
+  const bool keys = blockIdx.z == 0;
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
   // row block ranges
-  for (int rb = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; rb < pp.w.nrb; rb += gridDim.x * gridDim.y * 8) {
+  for (int rb = keys ? pp.w.nrb : (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; rb < pp.w.nrb; rb += gridDim.x * gridDim.y * 8) {
     constexpr int kRB = block_rows(D);
-    const int j0 = rb * kRB / p.G, j1 = min(p.C - 1, (int)(((int64_t)rb * kRB + kRB - 1) / p.G));
+    const int j0 = p.divG.div(rb * kRB), j1 = min(p.C - 1, p.divG.div(rb * kRB + kRB - 1));
     int lo = 0x7fffffff, hi = 0, lo_in = 0, hi_in = 0x7fffffff;
     for (int j = j0 + lane; j <= j1; j += 32) {
       int a, b;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
   const size_t ti = (size_t)kvh * pp.w.ntiles + tile;
   uint8_t* kt = ws + pp.w.oK + ti * Lay<D>::kTile;
   uint8_t* vt = ws + pp.w.oV + ti * Lay<D>::kTile;
-  if (tid < kBlk) {
+  if (keys && tid < kBlk) {
     float sk = 0.f, sv = 0.f;
     bool bad = false;
 #pragma unroll
@@ -214,38 +215,38 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
   const int sub = tid / D, c = tid % D;
 #pragma unroll
   for (int i0 = 0; i0 < kBlk; i0 += 4 * kAt) {
-    uint4 kx[4], vx[4];
+    uint4 x[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       int ph = -1;
 #pragma unroll
       for (int s = 0; s < kAt; ++s)
         if (i0 + u * kAt + s < kBlk && s == sub) ph = phys[(i0 + u * kAt + s) % kBlk];
-      kx[u] = vx[u] = make_uint4(0, 0, 0, 0);
-      if (ph >= 0) {
-        const size_t page = ((size_t)ph * p.Hkv + kvh) * (D * kBS);
-        kx[u] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + page) + c);
-        vx[u] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + page) + c);
-      }
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (ph >= 0)
+        x[u] = __ldg(reinterpret_cast<const uint4*>((keys ? p.k_cache : p.v_cache) + ((size_t)ph * p.Hkv + kvh) * (D * kBS)) + c);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + u * kAt + sub;
       if (i >= kBlk) continue;
-      const int dc = c / kBS, key = i * kBS + c % kBS;
-      uint8_t* atom = kt + (size_t)(dc / 4) * (kKeys * 128);
-      *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4))) =
-          make_uint4(bf16x2_codes(kx[u].x, 0), bf16x2_codes(kx[u].x, 2), bf16x2_codes(kx[u].y, 0), bf16x2_codes(kx[u].y, 2));
-      *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4) + 1)) =
-          make_uint4(bf16x2_codes(kx[u].z, 0), bf16x2_codes(kx[u].z, 2), bf16x2_codes(kx[u].w, 0), bf16x2_codes(kx[u].w, 2));
-      uint8_t* half = vt + (size_t)(i / 4) * (D * 128);
-      uint4 h0, h1;
-      s8x4_to_f16(vx[u].x, h0.x, h0.y);
-      s8x4_to_f16(vx[u].y, h0.z, h0.w);
-      s8x4_to_f16(vx[u].z, h1.x, h1.y);
-      s8x4_to_f16(vx[u].w, h1.z, h1.w);
-      *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4))) = h0;
-      *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4) + 1)) = h1;
+      if (keys) {
+        const int dc = c / kBS, key = i * kBS + c % kBS;
+        uint8_t* atom = kt + (size_t)(dc / 4) * (kKeys * 128);
+        *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4))) =
+            make_uint4(bf16x2_codes(x[u].x, 0), bf16x2_codes(x[u].x, 2), bf16x2_codes(x[u].y, 0), bf16x2_codes(x[u].y, 2));
+        *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4) + 1)) =
+            make_uint4(bf16x2_codes(x[u].z, 0), bf16x2_codes(x[u].z, 2), bf16x2_codes(x[u].w, 0), bf16x2_codes(x[u].w, 2));
+      } else {
+        uint8_t* half = vt + (size_t)(i / 4) * (D * 128);
+        uint4 h0, h1;
+        s8x4_to_f16(x[u].x, h0.x, h0.y);
+        s8x4_to_f16(x[u].y, h0.z, h0.w);
+        s8x4_to_f16(x[u].z, h1.x, h1.y);
+        s8x4_to_f16(x[u].w, h1.z, h1.w);
+        *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4))) = h0;
+        *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4) + 1)) = h1;
+      }
     }
   }
 }
@@ -276,12 +277,8 @@ __device__ __forceinline__ bool walk_next(const Params& pp, const Range* rg, Wal
   return true;
 }
 
-// The cut of `total` steps over `grid` CTAs: the first total % grid take one more.
-__host__ __device__ __forceinline__ int cut_at(int total, int grid, int c) { return total / grid * c + min(c, total % grid); }
-__device__ __forceinline__ int cta_of(int total, int grid, int u) {
-  const int per = total / grid, rem = total % grid, big = rem * (per + 1);
-  return u < big ? u / (per + 1) : rem + (u - big) / per;
-}
+// The cut of the list over the CTAs: `per` steps each, the first `rem` one more.
+__device__ __forceinline__ int cut_at(int per, int rem, int c) { return per * c + min(c, rem); }
 
 // Bounded wait that gives up at once when the CTA has aborted (error 1 after the
 // time limit); every thread still runs its loops and barriers.
@@ -430,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
     per_head += scan_step(rb < pp.w.nrb ? rg[rb].hi - rg[rb].lo : 0, before);
   }
   const int total = per_head * p.Hkv;
-  const int u0 = uni(cut_at(total, grid, blockIdx.x)), u1 = uni(cut_at(total, grid, blockIdx.x + 1));
+  const int per = p.divGrid.div(total), rem = total - per * grid;
+  const int u0 = uni(cut_at(per, rem, blockIdx.x)), u1 = uni(cut_at(per, rem, blockIdx.x + 1));
   if (tid < 2) scan[16 + tid] = 0;
   const int kvh0 = per_head > 0 ? u0 / per_head : 0;
   {
@@ -460,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
     h.kvh = w.kvh;
     h.first = w.first;
     h.cnt = w.cnt;
-    h.total = total;
+    h.per = per;
+    h.rem = rem;
     reinterpret_cast<Head*>(ws + pp.w.oHead)[blockIdx.x] = h;
   }
   // row blocks without a visible key: zero rows
@@ -1035,33 +1034,45 @@ __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_co
   if (h.rb < 0 || h.first == 0) return;
   const int row = part * 32 + lane, R = p.C * p.G;
   if (h.rb * kRB + part * 32 >= R) return;
-  const int grid = pp.w.grid, total = h.total;
-  const int a = cut_at(total, grid, cut) - h.first, e = a + h.cnt;
-  const int c0 = cta_of(total, grid, a), c1 = cta_of(total, grid, e - 1);
-  if (cut != c0 + 1) return;
+  const int per = h.per, rem = h.rem;
+  const int a = cut_at(per, rem, cut) - h.first, e = a + h.cnt, c0 = cut - 1;
+  if (cut_at(per, rem, c0) > a) return;  // not the first cut of the row block
+  const bool own0 = cut_at(per, rem, c0) == a;
+  int c1 = cut;  // the last CTA that starts before the row block's end
+  while (c1 + 1 < pp.w.grid && cut_at(per, rem, c1 + 1) < e) ++c1;
   float4 acc[kQ];
   float M = -INFINITY, l = 0.f;
 #pragma unroll
   for (int i = 0; i < kQ; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0 + warp; c <= c1; c += 8) {
-    // a CTA whose range starts inside the row block has it as its first segment
-    const int slot = 2 * c + (cut_at(total, grid, c) >= a ? 0 : 1);
-    const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)slot * kRB * (D + 2);
-    float4 x[kQ];
+  for (int c = c0 + warp; c <= c1; c += 16) {
+    float4 x[2][kQ];
+    float m[2], ll[2];
 #pragma unroll
-    for (int i = 0; i < kQ; ++i) x[i] = *reinterpret_cast<const float4*>(rec + ((cg * kQ + i) * kRB + row) * 4);
-    const float m = rec[kRB * D + row], ll = rec[kRB * D + kRB + row];
-    const float nm = fmaxf(M, m);
-    if (nm != -INFINITY) {
-      const float f = ex2(M - nm), k = ex2(m - nm);
+    for (int k = 0; k < 2; ++k) {
+      const int cc = c + 8 * k;
+      m[k] = -INFINITY;
+      if (cc <= c1) {
+        // a CTA whose range starts inside the row block has it as its first segment
+        const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)(2 * cc + (cc > c0 || own0 ? 0 : 1)) * kRB * (D + 2);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) x[k][i] = *reinterpret_cast<const float4*>(rec + ((cg * kQ + i) * kRB + row) * 4);
+        m[k] = rec[kRB * D + row];
+        ll[k] = rec[kRB * D + kRB + row];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (m[k] == -INFINITY) continue;
+      const float nm = fmaxf(M, m[k]);
+      const float f = ex2(M - nm), g = ex2(m[k] - nm);
 #pragma unroll
       for (int i = 0; i < kQ; ++i) {
-        acc[i].x = acc[i].x * f + x[i].x * k;
-        acc[i].y = acc[i].y * f + x[i].y * k;
-        acc[i].z = acc[i].z * f + x[i].z * k;
-        acc[i].w = acc[i].w * f + x[i].w * k;
+        acc[i].x = acc[i].x * f + x[k][i].x * g;
+        acc[i].y = acc[i].y * f + x[k][i].y * g;
+        acc[i].z = acc[i].z * f + x[k][i].z * g;
+        acc[i].w = acc[i].w * f + x[k][i].w * g;
       }
-      l = l * f + ll * k;
+      l = l * f + ll[k] * g;
       M = nm;
     }
   }
@@ -1091,7 +1102,8 @@ __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_co
       o = __fmaf_rn(s_o[k][rr][lane], f, o);
     }
     const float v = den > 0.f ? o / den : 0.f;
-    store_out1(p.out, p.out_bf16, ((size_t)(r / p.G) * p.Hq + h.kvh * p.G + r % p.G) * D + cg * kMergeCols + lane, v);
+    const int j = p.divG.div(r);
+    store_out1(p.out, p.out_bf16, ((size_t)j * p.Hq + h.kvh * p.G + r - j * p.G) * D + cg * kMergeCols + lane, v);
   }
 }
 
@@ -1107,7 +1119,7 @@ cudaError_t launch(const Params& pp, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) opted[dev] = true;
   }
-  cudaError_t e = launch_pdl(block_tiles_kernel<D>, dim3(pp.w.ntiles, pp.a.Hkv), dim3(256), 0, stream, pp);
+  cudaError_t e = launch_pdl(block_tiles_kernel<D>, dim3(pp.w.ntiles, pp.a.Hkv, 2), dim3(256), 0, stream, pp);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(pp.w.grid), dim3(kThreads), Lay<D>::kTotal, stream, pp);
   if (e != cudaSuccess || pp.w.grid == 1) return e;
