@@ -59,21 +59,22 @@ constexpr float kLazy = 8.0f;
 // each); 56 + 2 x 224 = 3 x 168, what 384 threads launch with.
 constexpr int kRegsCtl = 56, kRegsSoft = 224;
 static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * 168, "register split");
+constexpr int kSnap = 2;
 constexpr int kScales = 3 * kBlk;  // per tile: sK, log2 sV, 1 / sV of its blocks
 
-// The workspace (all offsets multiples of 128 bytes).
+// The workspace (all offsets multiples of 128 bytes): where every CTA's range
+// starts (cuts [grid + 1] and a header each), the row blocks' ranges, the operand
+// tiles and their scales, the records.
 struct Head {
-  int rb, kvh, first, cnt;  // where a CTA's range starts: row block (-1: empty range), KV head, tile, tiles
-  int per, rem, pad[2];     // the cut of the list (cut_at)
+  int rb, kvh, first, cnt;  // row block, KV head, tiles of the row block before the range, its tiles
 };
-static_assert(sizeof(Head) == 32, "");
 struct Range {
   int lo, hi;        // the row block's tiles
   int lo_in, hi_in;  // keys that every row of it sees
 };
 struct Plan {
   int nrb, tile0, ntiles, grid;
-  size_t oHead, oRange, oScale, oK, oV, oRec, bytes;
+  size_t oCuts, oHead, oRange, oScale, oK, oV, oRec, bytes;
 };
 inline Plan plan_of(int H, int C, int G, int Hkv, int D, int window, int grid) {
   Plan p;
@@ -84,8 +85,9 @@ inline Plan plan_of(int H, int C, int G, int Hkv, int D, int window, int grid) {
   p.ntiles = (H + C + kKeys - 1) / kKeys - p.tile0;
   p.grid = grid;
   const size_t tile = (size_t)kKeys * D * 2, n = (size_t)p.ntiles * Hkv;
-  p.oHead = 0;
-  p.oRange = up(sizeof(Head) * grid);
+  p.oCuts = 0;
+  p.oHead = up(sizeof(int) * ((size_t)grid + 1));
+  p.oRange = p.oHead + up(sizeof(Head) * (size_t)grid);
   p.oScale = p.oRange + up(sizeof(Range) * (size_t)p.nrb);
   p.oK = p.oScale + up(n * kScales * 4);
   p.oV = p.oK + n * tile;
@@ -428,40 +430,60 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
   }
   const int total = per_head * p.Hkv;
   const int per = p.divGrid.div(total), rem = total - per * grid;
-  const int u0 = uni(cut_at(per, rem, blockIdx.x)), u1 = uni(cut_at(per, rem, blockIdx.x + 1));
-  if (tid < 2) scan[16 + tid] = 0;
-  const int kvh0 = per_head > 0 ? u0 / per_head : 0;
+  int u[2], kvh[2];  // the range's ends: place in the list, KV head
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    u[e] = cut_at(per, rem, blockIdx.x + e);
+    kvh[e] = u[e] < total ? u[e] / per_head : 0;
+  }
+  if (tid < 6) scan[16 + tid] = 0;  // row block, tile in it, its tiles
   {
-    int run = kvh0 * per_head;
+    int run = 0;
     for (int r0 = 0; r0 < pp.w.nrb; r0 += kThreads) {
       const int rb = r0 + tid;
       const int cnt = rb < pp.w.nrb ? rg[rb].hi - rg[rb].lo : 0;
       const int sum = scan_step(cnt, before);
-      const int s0 = run + before;
-      if (u0 >= s0 && u0 < s0 + cnt) {
-        scan[16] = rb;
-        scan[17] = u0 - s0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int in = u[e] - kvh[e] * per_head - (run + before);
+        if (u[e] < total && in >= 0 && in < cnt) {
+          scan[16 + 3 * e] = rb;
+          scan[17 + 3 * e] = in;
+          scan[18 + 3 * e] = cnt;
+        }
       }
       run += sum;
     }
   }
   __syncthreads();
+  // A cut near the border of two row blocks moves there, by up to kSnap tiles: a
+  // segment more costs its CTA about as much, and its record is written and merged.
   Walk w;
-  w.kvh = kvh0;
-  w.rb = uni(scan[16]);
-  w.first = uni(scan[17]);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int in = scan[17 + 3 * e], cnt = scan[18 + 3 * e], reach = min(kSnap, (per + 1) / 2);
+    int first = in;
+    if (u[e] > 0 && u[e] < total) {
+      if (in <= reach) first = 0;
+      else if (cnt - in <= reach) first = cnt;
+    }
+    u[e] = uni(u[e] + first - in);
+    if (e == 0) {
+      w.rb = uni(scan[16]);
+      w.first = uni(first);
+    }
+  }
+  const int u0 = u[0], u1 = u[1];
+  int* cuts = reinterpret_cast<int*>(ws + pp.w.oCuts);
+  if (tid == 0) {
+    cuts[blockIdx.x] = u0;
+    if (blockIdx.x + 1 == gridDim.x) cuts[gridDim.x] = u1;
+  }
+  w.kvh = uni(kvh[0]);
   w.left = u1 - u0;
   walk_load(rg, w);
-  if (tid == 0) {
-    Head h{};
-    h.rb = u0 < u1 ? w.rb : -1;
-    h.kvh = w.kvh;
-    h.first = w.first;
-    h.cnt = w.cnt;
-    h.per = per;
-    h.rem = rem;
-    reinterpret_cast<Head*>(ws + pp.w.oHead)[blockIdx.x] = h;
-  }
+  if (w.left > 0 && w.len == 0) walk_next(pp, rg, w);  // the range starts with the next row block
+  if (tid == 0) reinterpret_cast<Head*>(ws + pp.w.oHead)[blockIdx.x] = Head{w.rb, w.kvh, w.first, w.cnt};
   // row blocks without a visible key: zero rows
   for (int rb = blockIdx.x; rb < pp.w.nrb; rb += grid) {
     if (rg[rb].hi != rg[rb].lo) continue;
@@ -1030,16 +1052,18 @@ __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cg = blockIdx.x % kGroups, part = blockIdx.x / kGroups % kParts, cut = blockIdx.x / (kParts * kGroups) + 1;
   uint8_t* ws = static_cast<uint8_t*>(p.ws);
+  const int* cuts = reinterpret_cast<const int*>(ws + pp.w.oCuts);
+  const int here = cuts[cut], prev = cuts[cut - 1], after = cuts[cut + 1], grid = pp.w.grid, tid = threadIdx.x;
+  const int later = cut + 1 + tid < grid ? cuts[cut + 1 + tid] : 0x7fffffff;
   const Head h = reinterpret_cast<const Head*>(ws + pp.w.oHead)[cut];
-  if (h.rb < 0 || h.first == 0) return;
+  if (here >= after || h.first == 0) return;  // an empty range, or no row block is cut here
+  const int a = here - h.first, e = a + h.cnt, c0 = cut - 1;  // cuts inside a row block differ
+  if (prev > a) return;  // not the first cut of the row block
   const int row = part * 32 + lane, R = p.C * p.G;
   if (h.rb * kRB + part * 32 >= R) return;
-  const int per = h.per, rem = h.rem;
-  const int a = cut_at(per, rem, cut) - h.first, e = a + h.cnt, c0 = cut - 1;
-  if (cut_at(per, rem, c0) > a) return;  // not the first cut of the row block
-  const bool own0 = cut_at(per, rem, c0) == a;
-  int c1 = cut;  // the last CTA that starts before the row block's end
-  while (c1 + 1 < pp.w.grid && cut_at(per, rem, c1 + 1) < e) ++c1;
+  const bool own0 = prev == a;
+  int c1 = cut + __syncthreads_count(later < e);  // the last CTA that starts before the row block's end
+  for (int c = cut + 257; c < grid; c += 256) c1 += __syncthreads_count(c + tid < grid && cuts[c + tid] < e);
   float4 acc[kQ];
   float M = -INFINITY, l = 0.f;
 #pragma unroll
