@@ -55,9 +55,9 @@ constexpr int kThreads = 384;
 constexpr int kWG = 128;
 constexpr int kSoftWarp = 4;
 constexpr float kLazy = 8.0f;
-// Registers: 128 control threads at 56, 256 softmax threads at 224 (128 scores
-// each); 56 + 2 x 224 = 3 x 168, what 384 threads launch with.
-constexpr int kRegsCtl = 56, kRegsSoft = 224;
+// Registers: 128 control threads at 40, 256 softmax threads at 232 (128 scores
+// each); 40 + 2 x 232 = 3 x 168, what 384 threads launch with.
+constexpr int kRegsCtl = 40, kRegsSoft = 232;
 static_assert(kRegsCtl + 2 * kRegsSoft <= 3 * 168, "register split");
 constexpr int kSnap = 2;
 constexpr int kScales = 3 * kBlk;  // per tile: sK, log2 sV, 1 / sV of its blocks
