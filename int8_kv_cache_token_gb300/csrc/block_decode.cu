@@ -90,7 +90,7 @@ __device__ __forceinline__ void chunk_interval(const BlockDecodeParams& p, int j
   if (p.window > 0) lo = max(0, p.H + j - p.window + 1);
   if (p.key_begin != nullptr) lo = max(lo, p.key_begin[j]);
   hi = p.H + j + 1;
-  if (p.key_end != nullptr) hi = min(p.key_end[j], p.H + p.C);
+  if (p.key_end != nullptr) hi = max(0, min(p.key_end[j], p.H + p.C));
 }
 
 template <bool kChunk>

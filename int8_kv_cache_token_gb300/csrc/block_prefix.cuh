@@ -31,10 +31,22 @@
 // third kernel.  So a causal triangle, a window, packed documents and a short
 // chunk over a long history all fill the GPU.
 //
-// Warps: 0 tile copies, 1 MMA issue, 2 tensor memory, 4-7 and 8-11 softmax (and
-// the query rows).  One
-// thread issues both products: MMAs of a CTA execute in
-// issue order, which is what lets W share its S slot with the S after next.
+// Warps: 0 tile copies, 1 MMA issue, 2 tensor memory, 4-7 and 8-11 softmax and
+// query rows.  One thread issues both products: MMAs of a CTA execute in issue
+// order, which is what lets W share its S slot with the S after next.
+//
+// What bounds it, measured on a GB300 (2048 rows over 16384 keys).  24/4 heads of
+// 256: 550 us, 1590 TFLOP/s, 0.81 of the dense peak; a tile's products want 2048
+// cycles and take about 2600, because Q K^T with both operands in shared memory
+// reads 128 bytes a cycle, all that shared memory gives, beside the tile copies.
+// With a cap 672 us: the polynomial makes the softmax of a tile (3900 cycles) the
+// longest part of the S -> W -> O chain, of which two are in flight.  32/8 heads of
+// 128: 442 us, 1320 TFLOP/s: the chain again, 1024 cycles of exponentials (16 a
+// cycle) for 1024 cycles of products.  Tried and dropped: exponentials of one pair
+// in four by a polynomial (FMA issue was the next limit: 520 against 462 us at
+// head_dim 128), and the maximum, the scores and the weights in one pass that is
+// repeated when the maximum moves (its branches keep the compiler from overlapping
+// the 32-column steps: 594 against 550 us at 256, 592 against 442 us at 128).
 #pragma once
 
 #include <type_traits>
@@ -133,7 +145,7 @@ __device__ __forceinline__ void interval(const BlockDecodeParams& p, int j, int&
   if (p.window > 0) lo = max(0, p.H + j - p.window + 1);
   if (p.key_begin != nullptr) lo = max(lo, p.key_begin[j]);
   hi = p.H + j + 1;
-  if (p.key_end != nullptr) hi = min(p.key_end[j], p.H + p.C);
+  if (p.key_end != nullptr) hi = max(0, min(p.key_end[j], p.H + p.C));
 }
 
 __device__ __forceinline__ uint32_t bf16x2_codes(uint32_t w, int i) {

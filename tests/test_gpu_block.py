@@ -347,6 +347,61 @@ def test_chunk_hidden_blocks_and_bad_tables():
         assert i8.device_error() == 2
 
 
+def test_chunk_intervals_at_the_ends_of_their_type():
+    """Begins and ends anywhere in 32 bits: cut to the keys there are."""
+    big = 2 ** 31 - 1
+
+    def begin(rng, pos):
+        return rng.choice([-big - 1, -1, 0, 7, big], pos.size)
+
+    def end(rng, pos):
+        return rng.choice([-big - 1, -1, 0, 20, big], pos.size)
+
+    for D, C in ((64, 5), (64, 90), (256, 70)):
+        _chunk(D, 4, 2, 60, C, torch.float32, seed=C, begin=begin, end=end)
+        _chunk(D, 4, 2, 60, C, seed=C, end=end, window=30, slopes=True)
+
+
+def test_chunk_many_row_blocks():
+    """More row blocks than the threads that lay out the work."""
+    _chunk(64, 8, 1, 100, 12400, seed=3, window=64, sample=12)
+
+
+def test_pool_beyond_32_bits():
+    """Blocks whose codes lie past 2^32 bytes of the pool."""
+    rng = np.random.default_rng(40)
+    Hq, Hkv, D, C = 8, 8, 256, 40
+    NB = (1 << 32) // (Hkv * D * BS) + 50
+    small, _ = tables(rng, [C], extra=0)
+    n = small.shape[1]
+    c = Cache(n, Hkv, D)  # zeros, like the pool
+    g = dict(k_cache=torch.zeros((NB, Hkv, D // 16, 16, 16), dtype=torch.int8, device="cuda"),
+             v_cache=torch.zeros((NB, Hkv, D, 16), dtype=torch.int8, device="cuda"),
+             k_scale=torch.zeros((NB, Hkv), device="cuda"), v_scale=torch.zeros((NB, Hkv), device="cuda"))
+    table = np.int32(NB - 40 + small)
+    x = {w: bf16(rng.standard_normal((C, Hkv, D))) for w in "kv"}
+    q = bf16(rng.standard_normal((C, Hq, D)))
+    i8.block_kv_write(dev_bf16(x["k"]), dev_bf16(x["v"]), dev(np.int32([C])), dev(table), **g, cu_tokens=cu_of([C]))
+    c.write(x, [C], [C], small)
+    for name, part in upload(c).items():
+        assert torch.equal(g[name][NB - 40:NB - 40 + n], part)
+    k = torch.empty((C, Hkv, D), device="cuda")
+    v = torch.empty_like(k)
+    i8.block_kv_read(k, v, dev(np.int32([C])), dev(table), **g, cu_tokens=cu_of([C]))
+    assert np.array_equal(k.cpu().numpy(), c.history(small[0], C, "k"))
+    for rows in (1, C):  # the decode, and a chunk of as many rows on either route
+        pos = np.arange(C - rows, C)
+        ref, err = attend(q[C - rows:], c, small[0], C, 0 * pos, pos + 1, pos, D ** -0.5, 0.0, None, False)
+        out = torch.empty((rows, Hq, D), device="cuda")
+        i8.block_prefix_attn(out, dev_bf16(q[C - rows:]), **g, block_table=dev(table[0]), history_len=C - rows)
+        close(out, ref, err, False)
+    out = torch.empty((1, Hq, D), device="cuda")
+    i8.block_decode_attn(out, dev_bf16(q[C - 1:]), **g, block_tables=dev(table), seq_lens=dev(np.int32([C])))
+    ref, err = attend(q[C - 1:], c, small[0], C, [0], [C], [C - 1], D ** -0.5, 0.0, None, False)
+    close(out, ref, err, False)
+    assert i8.device_error() == 0
+
+
 def test_chunk_rows_at_the_limits_of_both_routes():
     """Numbers of (token, head) rows around the change of route and around a row block."""
     for C in (63, 64, 65, 127, 128, 129):
