@@ -473,8 +473,9 @@ i8kv_status i8kv_block_kv_read(void* k_out, void* v_out, int out_dtype, int T, c
 /* outputs 12.  V scales below 2^-100 count as 2^-100.                          */
 /* workspace: at least i8kv_block_decode_workspace_bytes(...) bytes, 16-byte   */
 /* aligned, no initialization; the rules of the other decode calls apply        */
-/* (reuse on one stream; overlapping calls and graphs need their own).          */
-/* Two launches.                                                               */
+/* (reuse on one stream; overlapping calls and graphs need their own).  The    */
+/* size is 0, and workspace may be NULL, for calls that few SMs finish sooner:  */
+/* these take one launch, the others two.                                      */
 /* ------------------------------------------------------------------------ */
 size_t i8kv_block_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks);
 

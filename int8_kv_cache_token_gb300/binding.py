@@ -479,6 +479,13 @@ def _block_geom(k_cache, v_cache, k_scale, v_scale):
     """(addresses, NB, Hkv, D, device index) of a block-scaled cache."""
     NB, Hkv, D = _cache_geom(k_cache, 16)
     dev = k_cache.get_device()
+    scales = (NB, Hkv)
+    if (k_cache.dtype is _i8 and v_cache.dtype is _i8 and k_scale.dtype is _f32 and v_scale.dtype is _f32
+            and dev == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() and dev >= 0
+            and v_cache.shape == (NB, Hkv, D, BLOCK_SIZE) and k_scale.shape == scales and v_scale.shape == scales
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()), NB, Hkv, D, dev
+    # something is off: which, and how
     _require(dev >= 0, "k_cache must be a CUDA tensor")
     return (_at(k_cache, _i8, k_cache.shape, dev, "k_cache"), _at(v_cache, _i8, (NB, Hkv, D, BLOCK_SIZE), dev, "v_cache"),
             _at(k_scale, _f32, (NB, Hkv), dev, "k_scale"), _at(v_scale, _f32, (NB, Hkv), dev, "v_scale")), NB, Hkv, D, dev
@@ -503,7 +510,8 @@ def _call(fn, dev: int, stream, *args):
 def _ragged(seq_lens, block_tables, cu_tokens, T, dev):
     _require(block_tables.dim() == 2, "block_tables must be [B, max_blocks]")
     B, mb = block_tables.shape
-    _require(cu_tokens is not None or T == B, f"{T} rows for {B} sequences need cu_tokens")
+    if cu_tokens is None and T != B:
+        raise I8KVError(ERR_INVALID_ARG, f"{T} rows for {B} sequences need cu_tokens")
     return (_at(cu_tokens, _i32, (B + 1,), dev, "cu_tokens"), _at(seq_lens, _i32, (B,), dev, "seq_lens"),
             _at(block_tables, _i32, block_tables.shape, dev, "block_tables"), B, mb)
 
@@ -550,13 +558,15 @@ def _cuda(dev: int) -> torch.device:
 def _block_bytes(name: str, dev: int, *shape) -> int:
     """A workspace size: it depends on the shape and the device's number of SMs alone."""
     with torch.cuda.device(dev):
-        return max(int(getattr(lib(), name)(*shape)), 16)
+        return int(getattr(lib(), name)(*shape))
 
 
 def _workspace(workspace, dev: int, stream, name: str, *shape):
-    """(tensor, bytes): the given workspace, or one allocated for this call on its stream."""
+    """(tensor, bytes): the given workspace, or one allocated for this call on its stream (None where it needs none)."""
     if workspace is None:
         n = _block_bytes(name, dev, *shape)
+        if n == 0:
+            return None, 0
         if stream is None:
             return torch.empty(n, dtype=torch.uint8, device=_cuda(dev)), n
         with torch.cuda.stream(stream):
@@ -573,7 +583,9 @@ def _device_index(device) -> int:
 
 def block_decode_workspace(B: int, Hq: int, Hkv: int, D: int, max_blocks: int, device="cuda") -> torch.Tensor:
     """A block_decode_attn workspace (reusable by later calls on the same stream)."""
-    return _workspace(None, _device_index(device), None, "i8kv_block_decode_workspace_bytes", B, Hq, Hkv, D, max_blocks)[0]
+    dev = _device_index(device)
+    return torch.empty(max(_block_bytes("i8kv_block_decode_workspace_bytes", dev, B, Hq, Hkv, D, max_blocks), 16),
+                       dtype=torch.uint8, device=_cuda(dev))
 
 
 def block_decode_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, workspace=None,
@@ -587,8 +599,9 @@ def block_decode_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, 
     on.  workspace: a block_decode_workspace(...) tensor; when None one is allocated for this call."""
     cache, NB, Hkv, D, dev = _block_geom(k_cache, v_cache, k_scale, v_scale)
     _require(q.dim() == 3, "q must be [B, Hq, D]")
-    B, Hq, _ = shape = q.shape
-    _require(shape[2] == D, f"q has head_dim {shape[2]}, the cache {D}")
+    B, Hq, Dq = shape = q.shape
+    if Dq != D:
+        raise I8KVError(ERR_INVALID_ARG, f"q has head_dim {Dq}, the cache {D}")
     qp, qs = _rows(q, shape, dev, "q")
     code = _out_code(out)
     op = _at(out, out.dtype, shape, dev, "out")
@@ -597,13 +610,14 @@ def block_decode_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, 
     al = _at(alibi_slopes, _f32, (Hq,), dev, "alibi_slopes")
     ws, n = _workspace(workspace, dev, stream, "i8kv_block_decode_workspace_bytes", B, Hq, Hkv, D, mb)
     _call(lib().i8kv_block_decode_attn, dev, stream, op, code, qp, qs, *cache, bt, sl, kb, al, B, Hq, Hkv, D, BLOCK_SIZE,
-          mb, NB, softmax_scale, softcap, window, ws.data_ptr(), n)
+          mb, NB, softmax_scale, softcap, window, None if ws is None else ws.data_ptr(), n)
 
 
 def block_prefix_workspace(history_len: int, chunk_len: int, Hq: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
     """A block_prefix_attn workspace (reusable by later calls on the same stream)."""
-    return _workspace(None, _device_index(device), None, "i8kv_block_prefix_workspace_bytes", int(history_len), chunk_len, Hq,
-                      Hkv, D)[0]
+    dev = _device_index(device)
+    return torch.empty(max(_block_bytes("i8kv_block_prefix_workspace_bytes", dev, int(history_len), chunk_len, Hq, Hkv, D), 16),
+                       dtype=torch.uint8, device=_cuda(dev))
 
 
 def block_prefix_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_table, history_len: int, workspace=None,
@@ -630,4 +644,4 @@ def block_prefix_attn(out, q, k_cache, v_cache, k_scale, v_scale, block_table, h
     al = _at(alibi_slopes, _f32, (Hq,), dev, "alibi_slopes")
     ws, n = _workspace(workspace, dev, stream, "i8kv_block_prefix_workspace_bytes", history_len, C, Hq, Hkv, D)
     _call(lib().i8kv_block_prefix_attn, dev, stream, op, code, qp, qs, *cache, bt, history_len, C, kb, ke, al, Hq, Hkv, D,
-          BLOCK_SIZE, NB, softmax_scale, softcap, window, ws.data_ptr(), n)
+          BLOCK_SIZE, NB, softmax_scale, softcap, window, None if ws is None else ws.data_ptr(), n)

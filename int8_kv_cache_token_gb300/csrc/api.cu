@@ -657,7 +657,9 @@ static int head_passes(int Hq, int Hkv) { return (Hq / Hkv + 7) / 8; }
 
 size_t i8kv_block_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks) {
   if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || max_blocks <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
-  return i8kv::block_decode_workspace_bytes(D, i8kv::block_decode_grid(B, Hkv * head_passes(Hq, Hkv), max_blocks));
+  const int HH = Hkv * head_passes(Hq, Hkv);
+  if (i8kv::block_decode_cluster(D, B, HH, max_blocks)) return 0;
+  return i8kv::block_decode_workspace_bytes(D, i8kv::block_decode_grid(B, HH, max_blocks));
 }
 
 i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
@@ -684,9 +686,10 @@ i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, 
           "B=%d x %d head passes x max_blocks=%d: the block list is counted in 31 bits", B, p.HH, max_blocks);
   p.grid = i8kv::block_decode_grid(B, p.HH, max_blocks);
   p.divHG = i8kv::FastDiv((uint32_t)p.HG);
-  p.divGrid = i8kv::FastDiv((uint32_t)p.grid);
-  const size_t need = i8kv::block_decode_workspace_bytes(D, p.grid);
-  REQUIRE(workspace != nullptr && workspace_bytes >= need, I8KV_ERR_WORKSPACE,
+  p.cluster = i8kv::block_decode_cluster(D, B, p.HH, max_blocks);
+  p.divGrid = i8kv::FastDiv((uint32_t)(p.cluster ? p.HH : p.grid));
+  const size_t need = p.cluster ? 0 : i8kv::block_decode_workspace_bytes(D, p.grid);
+  REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need), I8KV_ERR_WORKSPACE,
           "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
   REQUIRE(aligned16(workspace), I8KV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   p.ws = workspace;
@@ -725,7 +728,7 @@ i8kv_status i8kv_block_prefix_attn(void* out, int out_dtype, const uint16_t* q, 
   p.H = history_len;
   p.C = chunk_len;
   const size_t need = i8kv::block_prefix_workspace_bytes(history_len, chunk_len, p.G, Hkv, D);
-  REQUIRE(workspace != nullptr && workspace_bytes >= need, I8KV_ERR_WORKSPACE,
+  REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need), I8KV_ERR_WORKSPACE,
           "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
   REQUIRE(aligned16(workspace), I8KV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   p.ws = workspace;

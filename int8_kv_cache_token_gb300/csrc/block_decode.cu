@@ -37,6 +37,8 @@ namespace {
 constexpr int kBS = 16;
 constexpr int kHeads = 8;        // query rows per pass: the MMA's N
 constexpr float kLazy = 8.0f;    // log2 units by which a score may pass M
+constexpr int kMaxCluster = 8;
+constexpr int kRounds = 6;       // most blocks per warp with a cluster per pair
 
 template <int D>
 struct Geo {
@@ -327,8 +329,35 @@ __device__ __forceinline__ uint32_t f16x2_rest(uint32_t hi, float a, float b) {
 }
 
 // kCap: scores pass through cap tanh(. / cap).  kHiLo: w as two f16 parts.
+// Shared memory of the cluster's CTA `rank`, and its barrier.
+__device__ __forceinline__ float4 peer_float4(const void* mine, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(smem_u32(mine)), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ float peer_float(const void* mine, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+               : "=f"(v)
+               : "r"(smem_u32(mine)), "r"(rank)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // kChunk: the work list holds the rows of one sequence's chunk.
-template <int D, bool kChunk, bool kCap, bool kHiLo>
+// kCluster: a cluster of p.cluster CTAs per pair instead of the evenly cut list.
+// The pair's blocks are shared out over the cluster, which joins its results
+// through distributed shared memory: no records, no second kernel, no look at the
+// other sequences' lengths.
+template <int D, bool kChunk, bool kCap, bool kHiLo, bool kCluster>
 __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(BlockDecodeParams p) {
   using Gm = Geo<D>;
   constexpr int NW = Gm::kWarps, NS = Gm::kStages;
@@ -352,6 +381,26 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   griddep_wait();
   griddep_launch_dependents();
 
+  Walk w;
+  const int cl_rank = kCluster ? (int)(blockIdx.x & (p.cluster - 1)) : 0;
+  if constexpr (kCluster) {
+    const int pair = blockIdx.x / p.cluster;  // a power of two
+    w.b = p.divGrid.div(pair);                // by HH
+    w.hh = pair - w.b * p.HH;
+    w.s = seq_of<kChunk>(p, w.b);
+    if (!kChunk && tid == 0 && cl_rank == 0 && w.hh == 0 && p.seq_lens[w.b] > p.max_blocks * kBS) record_error(2);
+    if (w.s.nb == 0) {  // the whole cluster leaves
+      if (cl_rank == 0)
+        for (int i = tid; i < kHeads * (D / 4); i += Gm::kThreads) {
+          int tok, hd;
+          if (row_of<kChunk>(p, w.b, w.hh, i / (D / 4), tok, hd))
+            store_out4(p.out, p.out_bf16, ((size_t)tok * p.Hq + hd) * D + (i % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+      return;
+    }
+    w.first = w.s.nb * cl_rank / p.cluster;
+    w.left = w.len = w.s.nb * (cl_rank + 1) / p.cluster - w.first;
+  } else {
   // ---- this CTA's range of the flattened list, and where it starts ----
   const Start at = find_start<kChunk, NW>(p, scan);
   if (!kChunk && blockIdx.x == 0)
@@ -369,7 +418,6 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   if (tid == 0) cuts_of(p)[blockIdx.x] = at.from.u;
   if (tid == 0 && blockIdx.x + 1 == gridDim.x) cuts_of(p)[gridDim.x] = at.to;
   if (at.from.u >= at.to) return;
-  Walk w;
   w.b = at.from.b;
   w.hh = at.from.hh;
   w.first = at.from.first;
@@ -379,6 +427,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   walk_segment(w);
   if (w.len == 0 && !walk_next<kChunk>(p, w)) return;  // the range starts with the next pair
   if (tid == 0) heads_of(p)[blockIdx.x] = Head{w.b, w.hh, w.first, w.s.nb};
+  }
 
   // The query rows of a segment as they are: row g, dims 16 i + 4 t4 .. + 3.
   uint2 raw[D / 16];
@@ -682,6 +731,52 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
       }
       __syncthreads();
     }
+    if constexpr (kCluster) {
+      // this CTA's sum in the first buffer, then every CTA joins a share of the columns
+      for (int i = tid; i < kHeads * D / 4; i += Gm::kThreads) {
+        float4* x = reinterpret_cast<float4*>(joined + i / (D / 4) * Gm::kRow + (i % (D / 4)) * 4);
+        float4 acc = *x;
+#pragma unroll 4
+        for (int k = 1; k < bufs; ++k) {
+          const float4 y = x[k * (kHeads * Gm::kRow / 4)];
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+        }
+        *x = acc;
+      }
+      cluster_sync();
+      for (int i = cl_rank * Gm::kThreads + tid; i < kHeads * D / 4; i += p.cluster * Gm::kThreads) {
+        const int h = i / (D / 4), c4 = (i % (D / 4)) * 4;
+        int tok, hd;
+        if (!row_of<kChunk>(p, w.b, w.hh, h, tok, hd)) continue;
+        float m[kMaxCluster], l = 0.f, C = -INFINITY;
+        float4 x[kMaxCluster], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < p.cluster) {
+            m[k] = peer_float(joint + h, k);
+            x[k] = peer_float4(joined + h * Gm::kRow + c4, k);
+            C = fmaxf(C, m[k]);
+          }
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+          if (k < p.cluster && m[k] != -INFINITY) {
+            const float f = ex2(m[k] - C);
+            l = __fmaf_rn(peer_float(joint + kHeads + h, k), f, l);
+            acc.x = __fmaf_rn(x[k].x, f, acc.x);
+            acc.y = __fmaf_rn(x[k].y, f, acc.y);
+            acc.z = __fmaf_rn(x[k].z, f, acc.z);
+            acc.w = __fmaf_rn(x[k].w, f, acc.w);
+          }
+        const float iv = l > 0.f ? 1.0f / l : 0.f;  // a row without a visible key is zero
+        store_out4(p.out, p.out_bf16, ((size_t)tok * p.Hq + hd) * D + c4,
+                   make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv));
+      }
+      cluster_sync();  // the peers have read this CTA's results
+      break;
+    }
     const bool whole = w.first == 0 && w.len == w.s.nb;
     float* rec = record(p, 2 * blockIdx.x + (first_seg ? 0 : 1), D);
     for (int i = tid; i < kHeads * D / 4; i += Gm::kThreads) {
@@ -808,9 +903,9 @@ __global__ void __launch_bounds__(D / 4 * kParts) block_decode_merge_kernel(Bloc
   }
 }
 
-template <int D, bool kChunk, bool kCap, bool kHiLo>
-cudaError_t launch_d(const BlockDecodeParams& p, cudaStream_t stream) {
-  auto* kernel = block_decode_kernel<D, kChunk, kCap, kHiLo>;
+template <int D, bool kChunk, bool kCap, bool kHiLo, bool kCluster>
+cudaError_t launch_c(const BlockDecodeParams& p, cudaStream_t stream) {
+  auto* kernel = block_decode_kernel<D, kChunk, kCap, kHiLo, kCluster>;
   // the shared-memory opt-in, once per device (graph captures then make no attribute call)
   int dev = 0;
   cudaGetDevice(&dev);
@@ -820,11 +915,32 @@ cudaError_t launch_d(const BlockDecodeParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) opted[dev] = true;
   }
+  if constexpr (kCluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.B * p.HH * p.cluster);
+    cfg.blockDim = dim3(Geo<D>::kThreads);
+    cfg.dynamicSmemBytes = Geo<D>::kTotal;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+  }
   const cudaError_t e = launch_pdl(kernel, dim3(p.grid), dim3(Geo<D>::kThreads), Geo<D>::kTotal, stream, p);
   if (e != cudaSuccess) return e;
   if (p.grid == 1) return cudaSuccess;
   const int rows = !kChunk && p.G < kHeads ? p.G : kHeads;
   return launch_pdl(block_decode_merge_kernel<D, kChunk>, dim3((p.grid - 1) * rows), dim3(D / 4 * kParts), 0, stream, p, rows);
+}
+
+template <int D, bool kChunk, bool kCap, bool kHiLo>
+cudaError_t launch_d(const BlockDecodeParams& p, cudaStream_t stream) {
+  return p.cluster ? launch_c<D, kChunk, kCap, kHiLo, true>(p, stream) : launch_c<D, kChunk, kCap, kHiLo, false>(p, stream);
 }
 
 template <int D, bool kChunk>
@@ -852,6 +968,52 @@ int block_decode_grid(int entries, int HH, int max_blocks) {
   const long long most = (long long)entries * HH * max_blocks;
   const int sms = block_device_sms();
   return most < sms ? (int)(most > 0 ? most : 1) : sms;
+}
+
+// How many clusters of c CTAs (one CTA per SM) run at once, asked once per device.
+static int clusters_at_once(int c) {
+  if (c == 1) return block_device_sms();
+  static int known[64][kMaxCluster + 1] = {};
+  int dev = 0, n = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return 0;
+  if (known[dev][c] > 0) return known[dev][c] - 1;
+  auto* kernel = block_decode_kernel<256, false, false, false, true>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMaxCluster * 64);
+  cfg.blockDim = dim3(Geo<256>::kThreads);
+  cfg.dynamicSmemBytes = Geo<256>::kTotal;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Geo<256>::kTotal) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev][c] = n + 1;
+  return n;
+}
+
+// CTAs per pair with a cluster per pair (0: the evenly cut list): the most that
+// run at once, if then no warp has more than kRounds blocks of the longest
+// sequence that the table can hold (a round takes about 1 us, the list's second
+// kernel and its look at all lengths about 3).  A call whose blocks the whole GPU
+// needs is better cut evenly, whatever the lengths.  Measured: one sequence of 4096
+// tokens (24/4/256) 10.1 us against 11.5 with the list, five of up to 777 (8/8/64)
+// 6.8 against 8.7.
+int block_decode_cluster(int D, int entries, int HH, int max_blocks) {
+  const long long pairs = (long long)entries * HH;
+  const int warps = D == 256 ? Geo<256>::kWarps : Geo<128>::kWarps;
+  static_assert(Geo<64>::kWarps == Geo<128>::kWarps, "");
+  int c = kMaxCluster;
+  while (c > 1 && pairs > clusters_at_once(c)) c >>= 1;
+  if (pairs > clusters_at_once(c)) return 0;
+  while (c > 1 && max_blocks <= (c / 2) * warps) c >>= 1;  // one round is enough
+  return max_blocks <= kRounds * c * warps ? c : 0;
 }
 
 size_t block_decode_workspace_bytes(int D, int grid) {

@@ -175,6 +175,7 @@ struct BlockDecodeParams {
   float cap_poly3[4];           // the same for |z| <= 1/2
   void* ws;
   int grid;
+  int cluster;      // CTAs per pair with a cluster per pair (divGrid is then by HH), 0: the evenly cut list
 };
 
 // Per-translation-unit device error words (read and cleared).
@@ -212,6 +213,7 @@ cudaError_t launch_block_kv_write(const BlockRaggedParams& r, const BlockWritePa
 cudaError_t launch_block_kv_read(const BlockRaggedParams& r, const BlockReadParams& p, cudaStream_t stream);
 int block_device_sms();
 int block_decode_grid(int entries, int HH, int max_blocks);
+int block_decode_cluster(int D, int entries, int HH, int max_blocks);
 size_t block_decode_workspace_bytes(int D, int grid);
 cudaError_t launch_block_decode(const BlockDecodeParams& p, cudaStream_t stream);
 // A chunk: few rows run in groups of eight (block_decode.cu), more in 128-row

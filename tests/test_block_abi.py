@@ -64,11 +64,15 @@ ATTN = [(dict(dt=3), 1, "out_dtype"), (dict(out=None), 1, "out is NULL"), (dict(
         (dict(qs=4), 1, "q_stride"), (dict(Hq=10), 1, "multiple"), (dict(Hq=0), 1, "multiple"), (dict(D=80), 2, "head_dim"),
         (dict(bs=32), 2, "block_size"), (dict(cap=-1.0), 1, "softcap"), (dict(cap=float("nan")), 1, "softcap"),
         (dict(cap=1e-5), 1, "softcap"), (dict(cap=float("inf")), 1, "softcap"), (dict(win=-1), 1, "window"),
-        (dict(kc=None), 1, "cache"), (dict(nb=0), 1, "num_blocks"), (dict(ws=None), 3, "workspace"), (dict(n=64), 3, "workspace"),
-        (dict(ws=P(24)), 1, "aligned"), (dict(Hq=8192), 2, "Hq")]
+        (dict(kc=None), 1, "cache"), (dict(nb=0), 1, "num_blocks"), (dict(Hq=8192), 2, "Hq")]
+# calls that need a workspace on every device
+BIG_DECODE = dict(B=1 << 16)
+BIG_CHUNK = dict(C=5000)
 
 
-@pytest.mark.parametrize("kw, status, word", ATTN + [(dict(sl=None), 1, "seq_lens"), (dict(mb=0), 1, "max_blocks"), (dict(B=-1), 1, "B=")])
+@pytest.mark.parametrize("kw, status, word", ATTN + [
+    (dict(sl=None), 1, "seq_lens"), (dict(mb=0), 1, "max_blocks"), (dict(B=-1), 1, "B="), (dict(B=1 << 28, mb=1 << 20), 2, "31 bits"),
+    (dict(BIG_DECODE, ws=None), 3, "workspace"), (dict(BIG_DECODE, n=64), 3, "workspace"), (dict(BIG_DECODE, ws=P(24)), 1, "aligned")])
 def test_decode_refusals(lib, kw, status, word):
     assert _decode(lib, **kw) == status
     assert word in _reason()
@@ -81,7 +85,10 @@ def _chunk(lib, out=A, dt=0, q=A, qs=24 * 256, kc=A, vc=A, sk=A, sv=A, bt=A, H=1
 
 
 @pytest.mark.parametrize("kw, status, word", ATTN + [(dict(bt=None), 1, "block_table"), (dict(H=-1), 1, "history_len"),
-                                                     (dict(C=-2), 1, "chunk_len"), (dict(H=1 << 30), 2, "history_len")])
+                                                     (dict(C=-2), 1, "chunk_len"), (dict(H=1 << 30), 2, "history_len"),
+                                                     (dict(BIG_CHUNK, ws=None), 3, "workspace"),
+                                                     (dict(BIG_CHUNK, n=64), 3, "workspace"),
+                                                     (dict(BIG_CHUNK, ws=P(24)), 1, "aligned")])
 def test_chunk_refusals(lib, kw, status, word):
     assert _chunk(lib, **kw) == status
     assert word in _reason()
@@ -90,8 +97,8 @@ def test_chunk_refusals(lib, kw, status, word):
 def test_empty_calls_and_workspace_sizes(lib):
     assert _decode(lib, B=0, ws=None) == 0 and _chunk(lib, C=0, ws=None, bt=None) == 0
     for D in (64, 128, 256):
-        assert lib.i8kv_block_decode_workspace_bytes(3, 24, 4, D, 100) > 0
-        assert lib.i8kv_block_prefix_workspace_bytes(0, 1, 24, 4, D) > 0
+        assert lib.i8kv_block_decode_workspace_bytes(1 << 16, 24, 4, D, 100) > 0
+        assert lib.i8kv_block_prefix_workspace_bytes(0, 5000, 24, 4, D) > 0
     assert lib.i8kv_block_decode_workspace_bytes(1, 24, 4, 96, 100) == 0
     assert lib.i8kv_block_decode_workspace_bytes(1, 23, 4, 128, 100) == 0
     assert lib.i8kv_block_prefix_workspace_bytes(-1, 5, 24, 4, 128) == 0

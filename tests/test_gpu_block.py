@@ -194,6 +194,28 @@ def test_decode_long_and_ragged():
     _decode(64, 2, 2, [int(x) for x in np.random.default_rng(0).integers(0, 40, 300)], seed=3)  # more sequences than threads
 
 
+def test_decode_work_split():
+    """A cluster per pair (narrow tables) and the evenly cut list (wide ones) on the same sequences, and clusters of which
+    some CTAs or warps have no block."""
+    rng = np.random.default_rng(11)
+    for D, Hq, Hkv, lens in ((256, 12, 2, [500, 3]), (128, 8, 2, [700, 0, 1, 260]), (64, 3, 1, [129]), (128, 40, 20, [90, 33, 5])):
+        table, nb = tables(rng, lens)
+        c = Cache(nb, Hkv, D).random(rng)
+        q = bf16(rng.standard_normal((len(lens), Hq, D)))
+        for mb in (table.shape[1], 40, 100, 400, 4000):
+            if mb < table.shape[1]:
+                continue
+            wide = np.full((len(lens), mb), nb + 5, np.int32)
+            wide[:, :table.shape[1]] = table
+            for dtype in (torch.float32, torch.bfloat16):
+                out = torch.full((len(lens), Hq, D), float("nan"), dtype=dtype, device="cuda")
+                i8.block_decode_attn(out, dev_bf16(q), **upload(c), block_tables=dev(wide), seq_lens=dev(np.int32(lens)))
+                for b, L in enumerate(lens):
+                    ref, err = attend(q[b:b + 1], c, table[b], L, [0], [L], [L - 1], D ** -0.5, 0.0, None, dtype is torch.bfloat16)
+                    close(out[b:b + 1], ref, err, dtype is torch.bfloat16)
+    assert i8.device_error() == 0
+
+
 def test_decode_extremes():
     """Scores far apart, and rows of q at the ends of bf16's range."""
     _decode(128, 4, 2, [200], torch.float32, seed=5, qmul=200.0)
@@ -308,6 +330,8 @@ def test_chunk_small(D, Hq, Hkv, H, C):
 def test_chunk_variants(D, kw):
     _chunk(D, 6, 2, 70, 41, seed=D, **kw)
     _chunk(D, 4, 4, 0, 130, seed=D + 1, **kw)
+    _chunk(D, 12, 2, 150, 41, seed=D + 2, **kw)
+    _chunk(D, 3, 1, 0, 150, torch.float32, seed=D + 3, **kw)
 
 
 @pytest.mark.parametrize("D, Hq, Hkv, H, C", [(64, 16, 2, 2900, 701), (128, 8, 4, 40, 2100), (256, 24, 4, 1000, 1300), (128, 32, 8, 9000, 33)])
@@ -357,7 +381,7 @@ def test_chunk_intervals_at_the_ends_of_their_type():
     def end(rng, pos):
         return rng.choice([-big - 1, -1, 0, 20, big], pos.size)
 
-    for D, C in ((64, 5), (64, 90), (256, 70)):
+    for D, C in ((64, 5), (64, 130), (256, 130)):
         _chunk(D, 4, 2, 60, C, torch.float32, seed=C, begin=begin, end=end)
         _chunk(D, 4, 2, 60, C, seed=C, end=end, window=30, slopes=True)
 
@@ -404,8 +428,12 @@ def test_pool_beyond_32_bits():
 
 def test_chunk_rows_at_the_limits_of_both_routes():
     """Numbers of (token, head) rows around the change of route and around a row block."""
-    for C in (63, 64, 65, 127, 128, 129):
-        _chunk(64, 2, 2, 77, C, torch.float32, seed=C)
+    for C in (63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257):
+        _chunk(64, 1, 1, 77, C, torch.float32, seed=C, sample=40)
+    # the same rows on either side of the rule on rows and keys, with and without a window
+    for H in (200, 3000):
+        for window in (0, 90):
+            _chunk(128, 8, 4, H, 40, seed=H, window=window)
 
 
 # ------------------------------------------------------------------------------------------------- together
@@ -554,5 +582,7 @@ def test_binding_refusals_on_device():
         i8.block_decode_attn(out.half(), q, **c, block_tables=bt, seq_lens=sl)
     with pytest.raises(i8.I8KVError, match="cover"):
         i8.block_prefix_attn(out, q, **c, block_table=bt[0], history_len=64)
+    n = 400  # more pairs than SMs: a call with a workspace
     with pytest.raises(i8.I8KVError, match="workspace"):
-        i8.block_decode_attn(out, q, **c, block_tables=bt, seq_lens=sl, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        i8.block_decode_attn(out.expand(n, 4, 64).contiguous(), q.expand(n, 4, 64), **c, block_tables=bt.expand(n, 4).contiguous(),
+                             seq_lens=sl.expand(n).contiguous(), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
