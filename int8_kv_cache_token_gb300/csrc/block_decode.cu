@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
   load_q(w);
 
   // ---- the page copies: a walk of their own, NS blocks ahead of the consumer ----
+  const uint64_t once = policy_evict_first();  // a page is read once a call
   Walk c = w;
   int c_i = warp;        // next block of the segment for this warp
   int c_n = 0;           // blocks asked for so far (slot c_n % NS)
@@ -486,8 +487,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) block_decode_kernel(Block
     if (lane == 0) mbar_expect_tx(&bar[slot], Gm::kStage);
     __syncwarp();
     if (lane == 0) {
-      bulk_g2s(ring + slot * Gm::kStage, p.k_cache + ph * Gm::kPage, Gm::kPage, &bar[slot]);
-      bulk_g2s(ring + slot * Gm::kStage + Gm::kPage, p.v_cache + ph * Gm::kPage, Gm::kPage, &bar[slot]);
+      bulk_g2s_hint(ring + slot * Gm::kStage, p.k_cache + ph * Gm::kPage, Gm::kPage, &bar[slot], once);
+      bulk_g2s_hint(ring + slot * Gm::kStage + Gm::kPage, p.v_cache + ph * Gm::kPage, Gm::kPage, &bar[slot], once);
     } else if (lane <= 2) {
       cp_async_4(lane == 1 ? &scl[slot].x : &scl[slot].y, (lane == 1 ? p.k_scale : p.v_scale) + ph, 4);
       cp_async_mbar_arrive(&bar[slot]);
