@@ -640,6 +640,8 @@ static i8kv_status block_attn_common(i8kv::BlockDecodeParams& p, void* out, int 
   for (int i = 0; i <= i8kv::kCapDeg; ++i) p.cap_poly[i] = tanh_poly[i] * p.cap_log2;
   static const float tanh_poly3[4] = {0.999999451f, -0.333262842f, 0.131899394f, -0.0443927384f};  // on [0, 1/4]: 6e-7
   for (int i = 0; i < 4; ++i) p.cap_poly3[i] = tanh_poly3[i] * p.cap_log2;
+  static const float tanh_poly2[3] = {0.999999603f, -0.33321897f, 0.128414339f};
+  for (int i = 0; i < 3; ++i) p.cap_poly2[i] = tanh_poly2[i] * p.cap_log2;
   return I8KV_OK;
 }
 

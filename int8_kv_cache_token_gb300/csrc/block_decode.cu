@@ -28,8 +28,9 @@
 // order.  Calls that few SMs finish sooner take a cluster per pair instead, joined
 // through distributed shared memory in the same launch.
 //
-// Bound by HBM: 16 sequences of 32768 tokens (32/8/128) 168 us, 6.4 TB/s, 0.94 of
-// the measured copy rate; 64 ragged ones (24/4/256, slopes) 348 us, 0.94.  One
+// Bound by HBM: 16 sequences of 32768 tokens (32/8/128) 164 us, 6.6 TB/s, 0.97 of
+// the measured copy rate; 64 ragged ones (24/4/256, slopes) 330 us, 0.99 (the page
+// copies' evict-first policy is worth 2 %).  One
 // sequence of 4096 (24/4/256) 10 us, all of it latency: lengths, table, pages, a
 // block's scores and products (0.8 us), the join.  A block of 16 tokens costs a
 // warp about 450 instructions at head_dim 256, a third of the issue slots at the

@@ -39,7 +39,7 @@
 // 256: 550 us, 1590 TFLOP/s, 0.81 of the dense peak; a tile's products want 2048
 // cycles and take about 2600, because Q K^T with both operands in shared memory
 // reads 128 bytes a cycle, all that shared memory gives, beside the tile copies.
-// With a cap 672 us: the polynomial makes the softmax of a tile (3900 cycles) the
+// With a cap 641 us: the polynomial makes the softmax of a tile (3700 cycles) the
 // longest part of the S -> W -> O chain, of which two are in flight.  32/8 heads of
 // 128: 442 us, 1320 TFLOP/s: the chain again, 1024 cycles of exponentials (16 a
 // cycle) for 1024 cycles of products.  Tried and dropped: exponentials of one pair
@@ -810,7 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
         if constexpr (kCap) {
           // z = score / cap; cap log2 e tanh z = z P(z^2), on the FMA pipes that the
           // exponentials leave idle: P interpolates tanh(z) / z at Chebyshev nodes, of
-          // degree 3 for |z| <= 1/2 (6e-7 relative; bf16 outputs) or 6 for |z| <= 1 (5e-8)
+          // degree 2 for |z| <= 1/4 and 3 for |z| <= 1/2 (4e-7 and 6e-7 relative; bf16
+          // outputs) or 6 for |z| <= 1 (5e-8)
           float zmax = 0.f;
 #pragma unroll
           for (int b = 0; b < kBlk; ++b) {
@@ -834,7 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1) block_prefix_kernel(const __grid_
                 f2_split(fma2(a, z, f2(addend(b, i - b * kBS), addend(b, i + 1 - b * kBS))), v[i], v[i + 1]);
               }
           };
-          if (!kHiLo && __all_sync(0xffffffffu, zmax <= 0.5f)) {
+          if (!kHiLo && __all_sync(0xffffffffu, zmax <= 0.25f)) {
+            poly(std::integral_constant<int, 2>{}, p.cap_poly2);
+          } else if (!kHiLo && __all_sync(0xffffffffu, zmax <= 0.5f)) {
             poly(std::integral_constant<int, 3>{}, p.cap_poly3);
           } else if (__all_sync(0xffffffffu, zmax <= 1.f)) {
             poly(std::integral_constant<int, kCapDeg>{}, p.cap_poly);

@@ -173,6 +173,7 @@ struct BlockDecodeParams {
   float cap_log2;   // the cap in log2 units, 0: none
   float cap_poly[kCapDeg + 1];  // cap_log2 tanh(z) = z P(z^2) for |z| <= 1
   float cap_poly3[4];           // the same for |z| <= 1/2
+  float cap_poly2[3];           // and for |z| <= 1/4
   void* ws;
   int grid;
   int cluster;      // CTAs per pair with a cluster per pair (divGrid is then by HH), 0: the evenly cut list
