@@ -73,6 +73,7 @@ i8kv_status i8kv_device_error(int* code) {
   int v = 0;
   cudaError_t (*readers[])(int*) = {i8kv::read_error_producer, i8kv::read_error_decode, i8kv::read_error_prefix,
                                     i8kv::read_error_block_cache, i8kv::read_error_block_decode,
+                                    i8kv::read_error_block_decode_wide,
                                     i8kv::read_error_block_prefix_64, i8kv::read_error_block_prefix_128,
                                     i8kv::read_error_block_prefix_256};
   for (auto rd : readers) {
@@ -655,13 +656,13 @@ static i8kv_status check_block_attn(int Hq, int Hkv, int D, int block_size, int 
   return I8KV_OK;
 }
 
-static int head_passes(int Hq, int Hkv) { return (Hq / Hkv + 7) / 8; }
+static int head_passes(int G, int R) { return (G + R - 1) / R; }
 
 size_t i8kv_block_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks) {
   if (B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || max_blocks <= 0 || (D != 64 && D != 128 && D != 256)) return 0;
-  const int HH = Hkv * head_passes(Hq, Hkv);
-  if (i8kv::block_decode_cluster(D, B, HH, max_blocks)) return 0;
-  return i8kv::block_decode_workspace_bytes(D, i8kv::block_decode_grid(B, HH, max_blocks));
+  const int G = Hq / Hkv, R = i8kv::block_decode_rows(D, G, B, Hkv, max_blocks), HH = Hkv * head_passes(G, R);
+  if (i8kv::block_decode_cluster(D, R, B, HH, max_blocks)) return 0;
+  return i8kv::block_decode_workspace_bytes(D, R, i8kv::block_decode_grid(B, HH, max_blocks));
 }
 
 i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, int64_t q_stride, const int8_t* k_cache,
@@ -682,20 +683,21 @@ i8kv_status i8kv_block_decode_attn(void* out, int out_dtype, const uint16_t* q, 
   p.key_begin = key_begin;
   p.B = B;
   p.max_blocks = max_blocks;
-  p.HG = head_passes(Hq, Hkv);
+  p.R = i8kv::block_decode_rows(D, p.G, B, Hkv, max_blocks);
+  p.HG = head_passes(p.G, p.R);
   p.HH = Hkv * p.HG;
   REQUIRE((int64_t)B * p.HH * max_blocks < (1ll << 31), I8KV_ERR_UNSUPPORTED,
           "B=%d x %d head passes x max_blocks=%d: the block list is counted in 31 bits", B, p.HH, max_blocks);
   p.grid = i8kv::block_decode_grid(B, p.HH, max_blocks);
   p.divHG = i8kv::FastDiv((uint32_t)p.HG);
-  p.cluster = i8kv::block_decode_cluster(D, B, p.HH, max_blocks);
+  p.cluster = i8kv::block_decode_cluster(D, p.R, B, p.HH, max_blocks);
   p.divGrid = i8kv::FastDiv((uint32_t)(p.cluster ? p.HH : p.grid));
-  const size_t need = p.cluster ? 0 : i8kv::block_decode_workspace_bytes(D, p.grid);
+  const size_t need = p.cluster ? 0 : i8kv::block_decode_workspace_bytes(D, p.R, p.grid);
   REQUIRE(need == 0 || (workspace != nullptr && workspace_bytes >= need), I8KV_ERR_WORKSPACE,
           "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
   REQUIRE(aligned16(workspace), I8KV_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
   p.ws = workspace;
-  return from_cuda(i8kv::launch_block_decode(p, static_cast<cudaStream_t>(stream)), "block decode launch");
+  return from_cuda(i8kv::launch_block_rows(p, false, static_cast<cudaStream_t>(stream)), "block decode launch");
 }
 
 size_t i8kv_block_prefix_workspace_bytes(int history_len, int chunk_len, int Hq, int Hkv, int D) {

@@ -9,18 +9,30 @@ cudaError_t launch_block_prefix_256(const bp::Params& pp, cudaStream_t stream);
 
 namespace {
 
-// Few (token, head) rows of a KV head run in groups of eight, each reading the
-// int8 cache itself; more run in 128-row blocks on 16-bit operand tiles, which
-// have to be made first.  With X = keys x Hkv x D in millions and g groups the
-// first takes about 6 + 0.4 g X us and the second 13 + 3.2 X (measured: 24/4/256,
-// 8192 keys, 60 rows 33 against 40 us, 126 rows 51 against 42; 1000 keys, 64 rows
-// 9 against 21, 126 rows 12 against 22).  More (group, KV head) pairs than SMs
-// pay for each pair's start and end instead (8/8/64, 64 keys, 192 rows: 34 against
-// 15 us), so beyond 64 rows the pairs have to fit.
+// Few (token, head) rows of a KV head run in groups of 8 or 16, each reading the int8
+// cache itself; more run in 128-row blocks on 16-bit operand tiles, which have to be
+// made first.  With X = keys x Hkv x D in millions and g groups of 16 the first takes
+// about 20 + 0.36 g X us and the second 24 + 2.05 X (measured: 24/4/256, 8192 keys, 60
+// rows 28 against 39 us, 96 rows 39 against 40, 126 rows 44 against 42; 32/8/128, 64
+// rows 30 against 43; 1000 keys, 256 rows 15 against 25).  More (group, KV head) pairs
+// than SMs pay for each pair's start and end instead (32/8/128, 384 rows without a
+// history 34 against 14 us), so beyond 64 rows the pairs have to fit.  The list of the
+// groups' blocks is counted in 31 bits.
+constexpr int kFewRows = 384;
 bool few_rows(int H, int C, int G, int Hkv, int D, int window) {
-  const int64_t groups = ((int64_t)C * G + 7) / 8;
+  const int64_t rows = (int64_t)C * G, groups = (rows + 15) / 16;
   const int64_t keys = window > 0 && (int64_t)window < H ? (int64_t)window + C : (int64_t)H + C;
-  return groups <= 8 || (groups <= 24 && groups * Hkv <= 128 && (groups - 8) * keys * Hkv * D <= 16000000);
+  if (2 * groups * Hkv * (((int64_t)H + C) / 16 + 1) >= (1ll << 31)) return false;
+  return groups <= 4 || (rows <= kFewRows && groups * Hkv <= 128 && (2 * groups - 11) * keys * Hkv * D <= 24000000);
+}
+
+// CTAs for the row groups: they see about the same keys, so where an equal number of
+// CTAs for each leaves few SMs over, no CTA has parts of two (and two joins).  That
+// is worth 4 us, and the idle SMs cost less up to some sixteen rounds of blocks over a
+// CTA's warps (16 pairs of 8192 keys, 32/8/128 24.0 -> 18.8 us; 32768 keys 43.2 -> 44.3).
+int group_grid(int pairs, int blocks) {
+  const int grid = block_decode_grid(pairs, 1, blocks), each = grid / pairs;
+  return 16 * pairs * each >= 15 * grid && blocks <= 128 * each ? pairs * each : grid;
 }
 
 int grid_of(const bp::Plan& w, int Hkv) {
@@ -34,9 +46,10 @@ int grid_of(const bp::Plan& w, int Hkv) {
 size_t block_prefix_workspace_bytes(int H, int C, int G, int Hkv, int D) {
   const int64_t rows = (int64_t)C * G;
   size_t n = 0;
-  if (rows <= 192) {  // a window may bring it to the groups of eight
-    const int groups = (int)((rows + 7) / 8), blocks = (H + C + 15) / 16;
-    n = block_decode_cluster(D, groups, Hkv, blocks) ? 0 : block_decode_workspace_bytes(D, block_decode_grid(groups, Hkv, blocks));
+  if (rows <= kFewRows) {  // a window may bring it to the row groups
+    const int blocks = (H + C + 15) / 16, R = block_decode_rows(D, (int)rows, 1, Hkv, blocks);
+    const int groups = ((int)rows + R - 1) / R;
+    n = block_decode_cluster(D, R, groups, Hkv, blocks) ? 0 : block_decode_workspace_bytes(D, R, group_grid(groups * Hkv, blocks));
     if (few_rows(H, C, G, Hkv, D, 0)) return n;
   }
   // without a window: the largest plan
@@ -47,14 +60,15 @@ size_t block_prefix_workspace_bytes(int H, int C, int G, int Hkv, int D) {
 cudaError_t launch_block_prefix(BlockDecodeParams p, cudaStream_t stream) {
   const int64_t rows = (int64_t)p.C * p.G;
   if (few_rows(p.H, p.C, p.G, p.Hkv, p.D, p.window)) {
-    p.B = (int)((rows + 7) / 8);
+    p.max_blocks = (p.H + p.C + 15) / 16;
+    p.R = block_decode_rows(p.D, (int)rows, 1, p.Hkv, p.max_blocks);
+    p.B = ((int)rows + p.R - 1) / p.R;
     p.HG = 1;
     p.HH = p.Hkv;
-    p.max_blocks = (p.H + p.C + 15) / 16;
-    p.grid = block_decode_grid(p.B, p.HH, p.max_blocks);
-    p.cluster = block_decode_cluster(p.D, p.B, p.HH, p.max_blocks);
+    p.grid = group_grid(p.B * p.HH, p.max_blocks);
+    p.cluster = block_decode_cluster(p.D, p.R, p.B, p.HH, p.max_blocks);
     p.divGrid = FastDiv((uint32_t)(p.cluster ? p.HH : p.grid));
-    return launch_block_chunk_rows(p, stream);
+    return launch_block_rows(p, true, stream);
   }
   bp::Params pp{p, bp::plan_of(p.H, p.C, p.G, p.Hkv, p.D, p.window, 1)};
   const int grid = grid_of(pp.w, p.Hkv);

@@ -164,9 +164,10 @@ struct BlockDecodeParams {
   const float* slopes;       // [Hq], nullable
   int B, Hq, Hkv, G, D, max_blocks, num_blocks, window;
   FastDiv divG, divHG, divGrid;  // by G, HG and grid
-  int HG, HH;       // passes of 8 query heads per KV head; Hkv * HG
-  // A chunk of one sequence (rows (token, head) of one KV head in groups of 8):
-  // B = ceil(C G / 8) groups, HH = Hkv, block_tables one row, seq_lens unused.
+  int R;            // query rows per pass: 8 or 16
+  int HG, HH;       // passes of R query heads per KV head; Hkv * HG
+  // A chunk of one sequence (rows (token, head) of one KV head in groups of R):
+  // B = ceil(C G / R) groups, HH = Hkv, block_tables one row, seq_lens unused.
   int H, C;
   const int32_t* key_end;    // [C], nullable: one past the last visible key
   float score_mul;  // q . k -> the score in log2 units (no cap) or score / cap
@@ -185,6 +186,7 @@ cudaError_t read_error_decode(int* value);
 cudaError_t read_error_prefix(int* value);
 cudaError_t read_error_block_cache(int* value);
 cudaError_t read_error_block_decode(int* value);
+cudaError_t read_error_block_decode_wide(int* value);
 cudaError_t read_error_block_prefix_64(int* value);
 cudaError_t read_error_block_prefix_128(int* value);
 cudaError_t read_error_block_prefix_256(int* value);
@@ -214,13 +216,16 @@ cudaError_t launch_block_kv_write(const BlockRaggedParams& r, const BlockWritePa
 cudaError_t launch_block_kv_read(const BlockRaggedParams& r, const BlockReadParams& p, cudaStream_t stream);
 int block_device_sms();
 int block_decode_grid(int entries, int HH, int max_blocks);
-int block_decode_cluster(int D, int entries, int HH, int max_blocks);
-size_t block_decode_workspace_bytes(int D, int grid);
-cudaError_t launch_block_decode(const BlockDecodeParams& p, cudaStream_t stream);
-// A chunk: few rows run in groups of eight (block_decode.cu), more in 128-row
+int block_decode_cluster(int D, int R, int entries, long long HH, int max_blocks);
+size_t block_decode_workspace_bytes(int D, int R, int grid);
+// Query rows per pass (8 or 16) where each of `entries` sequences has `rows` of them per KV head.
+int block_decode_rows(int D, int rows, int entries, int Hkv, int max_blocks);
+// Decode, or the row groups of a chunk.
+cudaError_t launch_block_rows(const BlockDecodeParams& p, bool chunk, cudaStream_t stream);
+cudaError_t launch_block_rows_wide(const BlockDecodeParams& p, bool chunk, cudaStream_t stream);
+// A chunk: few rows run in groups of 8 or 16 (block_decode.cuh), more in 128-row
 // blocks on the tensor cores (block_prefix.cuh).  p.grid and p.ws are set here.
 size_t block_prefix_workspace_bytes(int H, int C, int G, int Hkv, int D);
 cudaError_t launch_block_prefix(BlockDecodeParams p, cudaStream_t stream);
-cudaError_t launch_block_chunk_rows(const BlockDecodeParams& p, cudaStream_t stream);
 
 }  // namespace i8kv

@@ -99,6 +99,8 @@ def test_empty_calls_and_workspace_sizes(lib):
     for D in (64, 128, 256):
         assert lib.i8kv_block_decode_workspace_bytes(1 << 16, 24, 4, D, 100) > 0
         assert lib.i8kv_block_prefix_workspace_bytes(0, 5000, 24, 4, D) > 0
+        # few rows over so many keys that their list of blocks would pass 31 bits: as 128-row blocks, on 16-bit tiles
+        assert lib.i8kv_block_prefix_workspace_bytes((1 << 30) - 64, 8, 64, 64, D) > (1 << 30) * 64 * D * 4
     assert lib.i8kv_block_decode_workspace_bytes(1, 24, 4, 96, 100) == 0
     assert lib.i8kv_block_decode_workspace_bytes(1, 23, 4, 128, 100) == 0
     assert lib.i8kv_block_prefix_workspace_bytes(-1, 5, 24, 4, 128) == 0

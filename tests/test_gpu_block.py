@@ -153,9 +153,11 @@ def test_read_exact(D, Hkv, dtype):
 
 # ------------------------------------------------------------------------------------------------- decode
 def _decode(D, Hq, Hkv, lens, dtype=torch.bfloat16, cap=0.0, window=0, slopes=False, begin=None, seed=0, scale=0.0, zero=0.0,
-            spread=1.0, qmul=2.0, **kw):
+            spread=1.0, qmul=2.0, mb=0, **kw):
     rng = np.random.default_rng(seed)
     table, nb = tables(rng, lens)
+    if mb:  # a wider table, its rest outside the pool
+        table = np.concatenate([table, np.full((len(lens), mb - table.shape[1]), nb + 5, np.int32)], 1)
     c = Cache(nb, Hkv, D).random(rng, zero, spread)
     q = bf16(rng.standard_normal((len(lens), Hq, D)) * qmul)
     sl = np.exp2(-rng.uniform(0, 8, Hq)).astype(np.float32) if slopes else None
@@ -214,6 +216,21 @@ def test_decode_work_split():
                     ref, err = attend(q[b:b + 1], c, table[b], L, [0], [L], [L - 1], D ** -0.5, 0.0, None, dtype is torch.bfloat16)
                     close(out[b:b + 1], ref, err, dtype is torch.bfloat16)
     assert i8.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [9, 16, 20, 33])
+@pytest.mark.parametrize("kw", [dict(), dict(cap=1.5), dict(slopes=True, window=150, begin=[5, 0, 900, 60, 0, 0])])
+def test_decode_many_heads_per_kv_head(D, G, kw):
+    """More than eight query heads per KV head, in narrow tables (passes of eight rows) and wide ones (sixteen): full passes and
+    parts of one, CTAs with several segments, more sequences than a warp looks at together."""
+    for dtype in (torch.float32, torch.bfloat16):
+        _decode(D, 3 * G, 3, [400, 40, 1003, 77, 0, 1], dtype, seed=D + G, **kw)
+        _decode(D, 3 * G, 3, [400, 40, 1003, 77, 0, 1], dtype, seed=D + G, mb=2000, **kw)
+    _decode(D, G, 1, [90], seed=G, **{**kw, "begin": [3]})
+    if not kw:
+        _decode(D, 2 * G, 2, [900, 3], seed=G, mb=300, qmul=30.0)
+        _decode(D, G, 1, [int(x) for x in np.random.default_rng(G).integers(0, 60, 200)], seed=G, mb=500)
 
 
 def test_decode_extremes():
@@ -434,6 +451,25 @@ def test_chunk_rows_at_the_limits_of_both_routes():
     for H in (200, 3000):
         for window in (0, 90):
             _chunk(128, 8, 4, H, 40, seed=H, window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 31, 33, 64])
+def test_chunk_few_rows(D, rows):
+    """Around the numbers of rows that fill a pass of eight or sixteen, over short and long histories."""
+    for i, H in enumerate((0, 30, 2500, 41000)):
+        _chunk(D, 2, 2, H, rows, torch.float32 if i % 2 else torch.bfloat16, cap=3.0 if i else 0.0, begin=docs if i == 1 else None,
+               seed=D + rows, sample=6)
+        _chunk(D, 6, 2, H, (rows + 2) // 3, seed=D + rows, slopes=i == 2, begin=holes if i == 0 else None, sample=6)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kw", VARIANTS)
+def test_chunk_row_groups_of_sixteen(D, kw):
+    """A CTA per (group, KV head), and the evenly cut list of long histories."""
+    for dtype in (torch.float32, torch.bfloat16):
+        _chunk(D, 8, 8, 100, 235, dtype, seed=D, sample=40, **kw)
+        _chunk(D, 8, 4, 11000, 25, dtype, seed=D + 1, sample=10, **kw)
 
 
 # ------------------------------------------------------------------------------------------------- together
