@@ -1146,6 +1146,101 @@ __global__ void __launch_bounds__(256) block_prefix_merge_kernel(const __grid_co
   }
 }
 
+// The same for row blocks of a few records each: a warp has 32 rows and 32 columns
+// of its own, and goes through the records two at a time.
+template <int D>
+__global__ void __launch_bounds__(256) block_prefix_join_kernel(const __grid_constant__ Params pp) {
+  constexpr int kQ = kMergeCols / 4, kGroups = D / kMergeCols, kRB = block_rows(D), kSets = kRB / 32 * kGroups / 8;
+  const BlockDecodeParams& p = pp.a;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
+  const int cut = blockIdx.x / kSets + 1, set = blockIdx.x % kSets * 8 + warp;
+  const int cg = set % kGroups, part = set / kGroups;
+  uint8_t* ws = static_cast<uint8_t*>(p.ws);
+  const int* cuts = reinterpret_cast<const int*>(ws + pp.w.oCuts);
+  const int here = cuts[cut], prev = cuts[cut - 1], after = cuts[cut + 1], grid = pp.w.grid;
+  const int later = cut + 1 + tid < grid ? cuts[cut + 1 + tid] : 0x7fffffff;
+  const Head h = reinterpret_cast<const Head*>(ws + pp.w.oHead)[cut];
+  if (here >= after || h.first == 0) return;  // an empty range, or no row block is cut here
+  const int a = here - h.first, e = a + h.cnt, c0 = cut - 1;  // cuts inside a row block differ
+  if (prev > a) return;  // not the first cut of the row block
+  const bool own0 = prev == a;
+  int c1 = cut + __syncthreads_count(later < e);  // the last CTA that starts before the row block's end
+  for (int c = cut + 257; c < grid; c += 256) c1 += __syncthreads_count(c + tid < grid && cuts[c + tid] < e);
+  const int row = part * 32 + lane, r = h.rb * kRB + row, R = p.C * p.G;
+  if (r - lane >= R) return;
+  float4 acc[kQ];
+  float M = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kQ; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0; c <= c1; c += 2) {
+    float4 x[2][kQ];
+    float m[2], ll[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int cc = c + k;
+      m[k] = -INFINITY;
+      if (cc <= c1) {
+        // a CTA whose range starts inside the row block has it as its first segment
+        const float* rec = reinterpret_cast<const float*>(ws + pp.w.oRec) + (size_t)(2 * cc + (cc > c0 || own0 ? 0 : 1)) * kRB * (D + 2);
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) x[k][i] = *reinterpret_cast<const float4*>(rec + ((cg * kQ + i) * kRB + row) * 4);
+        m[k] = rec[kRB * D + row];
+        ll[k] = rec[kRB * D + kRB + row];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (m[k] == -INFINITY) continue;
+      const float nm = fmaxf(M, m[k]);
+      const float f = ex2(M - nm), g = ex2(m[k] - nm);
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        acc[i].x = acc[i].x * f + x[k][i].x * g;
+        acc[i].y = acc[i].y * f + x[k][i].y * g;
+        acc[i].z = acc[i].z * f + x[k][i].z * g;
+        acc[i].w = acc[i].w * f + x[k][i].w * g;
+      }
+      l = l * f + ll[k] * g;
+      M = nm;
+    }
+  }
+  const float iv = l > 0.f ? 1.0f / l : 0.f;
+  // 16-byte units, exchanged among the lanes of a group so that a row's line is whole
+  const int j = p.divG.div(r);
+  const size_t mine = r < R ? ((size_t)j * p.Hq + h.kvh * p.G + r - j * p.G) * D + cg * kMergeCols : ~(size_t)0;
+  auto put = [&](auto& u) {
+    constexpr int U = sizeof(u) / 16;
+    transpose_units<U>(u, lane);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)mine, (lane & ~(U - 1)) + k);
+      if (at == ~(size_t)0) continue;
+      if constexpr (U == 4)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at + lane % U * 8) = u[k];
+      else
+        *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at + lane % U * 4) = u[k];
+    }
+  };
+  if (p.out_bf16) {
+    uint4 u[kQ / 2];
+#pragma unroll
+    for (int i = 0; i < kQ / 2; ++i)
+      u[i] = make_uint4(bf16x2_rn(acc[2 * i].x * iv, acc[2 * i].y * iv), bf16x2_rn(acc[2 * i].z * iv, acc[2 * i].w * iv),
+                        bf16x2_rn(acc[2 * i + 1].x * iv, acc[2 * i + 1].y * iv),
+                        bf16x2_rn(acc[2 * i + 1].z * iv, acc[2 * i + 1].w * iv));
+    put(u);
+  } else {
+    uint4 u[kQ];
+#pragma unroll
+    for (int i = 0; i < kQ; ++i)
+      u[i] = make_uint4(__float_as_uint(acc[i].x * iv), __float_as_uint(acc[i].y * iv), __float_as_uint(acc[i].z * iv),
+                        __float_as_uint(acc[i].w * iv));
+    put(u);
+  }
+}
+
 template <int D, bool kCap, bool kSlope, bool kHiLo>
 cudaError_t launch(const Params& pp, cudaStream_t stream) {
   auto* kernel = block_prefix_kernel<D, kCap, kSlope, kHiLo>;
@@ -1162,7 +1257,14 @@ cudaError_t launch(const Params& pp, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(pp.w.grid), dim3(kThreads), Lay<D>::kTotal, stream, pp);
   if (e != cudaSuccess || pp.w.grid == 1) return e;
-  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * (block_rows(D) / 32) * (D / kMergeCols)), dim3(256), 0, stream, pp);
+  const int sets = (block_rows(D) / 32) * (D / kMergeCols);
+  // Up to some eight records a row block (on average; masks may leave one with more):
+  // a warp per 32 x 32 of it.  Row blocks 384 (24/4/256, 2048 rows over 16384 keys)
+  // 545 -> 517 us, 19 (16/1/128, 300 over 8192) 46 -> 42; 12 (24/4/256, 64 over 8192)
+  // 46 -> 47.5.
+  if ((int64_t)pp.w.nrb * pp.a.Hkv * 8 >= pp.w.grid)
+    return launch_pdl(block_prefix_join_kernel<D>, dim3((pp.w.grid - 1) * (sets / 8)), dim3(256), 0, stream, pp);
+  return launch_pdl(block_prefix_merge_kernel<D>, dim3((pp.w.grid - 1) * sets), dim3(256), 0, stream, pp);
 }
 
 template <int D, bool kHiLo>
