@@ -11,19 +11,24 @@ namespace {
 
 // Few (token, head) rows of a KV head run in groups of 8 or 16, each reading the int8
 // cache itself; more run in 128-row blocks on 16-bit operand tiles, which have to be
-// made first.  With X = keys x Hkv x D in millions and g groups of 16 the first takes
-// about 20 + 0.36 g X us and the second 24 + 2.05 X (measured: 24/4/256, 8192 keys, 60
-// rows 28 against 39 us, 96 rows 39 against 40, 126 rows 44 against 42; 32/8/128, 64
-// rows 30 against 43; 1000 keys, 256 rows 15 against 25).  More (group, KV head) pairs
-// than SMs pay for each pair's start and end instead (32/8/128, 384 rows without a
-// history 34 against 14 us), so beyond 64 rows the pairs have to fit.  The list of the
-// groups' blocks is counted in 31 bits.
+// made first.  Groups that have a cluster each take 8 to 20 us, less than the second
+// way's three launches (24/4/256, 1000 keys, 192 rows 14 against 20 us).  On the evenly
+// cut list, with X = keys x Hkv x D in millions and g groups of 16, they take about 20 +
+// 0.36 g X us against 23 + 1.55 X (24/4/256, 8192 keys, 60 rows 28 against 36 us, 96
+// rows 39 against 36.6; 32768 keys, 60 rows 66 against 77).  More (group, KV head) pairs
+// than SMs pay for each pair's start and end (32/8/128, 384 rows without a history 34
+// against 14 us), so beyond 64 rows the pairs have to fit.  The list of the groups'
+// blocks is counted in 31 bits.
 constexpr int kFewRows = 384;
 bool few_rows(int H, int C, int G, int Hkv, int D, int window) {
   const int64_t rows = (int64_t)C * G, groups = (rows + 15) / 16;
   const int64_t keys = window > 0 && (int64_t)window < H ? (int64_t)window + C : (int64_t)H + C;
   if (2 * groups * Hkv * (((int64_t)H + C) / 16 + 1) >= (1ll << 31)) return false;
-  return groups <= 4 || (rows <= kFewRows && groups * Hkv <= 128 && (2 * groups - 11) * keys * Hkv * D <= 24000000);
+  if (groups <= 4) return true;
+  if (rows > kFewRows) return false;
+  const int blocks = (H + C + 15) / 16, R = block_decode_rows(D, (int)rows, 1, Hkv, blocks);
+  if (block_decode_cluster(D, R, ((int)rows + R - 1) / R, Hkv, blocks)) return true;
+  return groups * Hkv <= 128 && (4 * groups - 17) * keys * Hkv * D <= 33000000;
 }
 
 // CTAs for the row groups: they see about the same keys, so where an equal number of

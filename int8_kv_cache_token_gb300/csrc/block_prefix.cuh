@@ -152,6 +152,26 @@ __device__ __forceinline__ uint32_t bf16x2_codes(uint32_t w, int i) {
   return bf16x2_rn((float)(int8_t)((w >> (8 * i)) & 0xffu), (float)(int8_t)((w >> (8 * i + 8)) & 0xffu));
 }
 
+// Chunks 2 q and 2 q + 1 of a row of swizzled 128-byte rows: one 32-byte sector,
+// written whole where the workspace allows it.  By halves it is two partial writes:
+// 18432 keys, 4 KV heads of 256: 18.3 us, 6.2 TB/s read and written, against 30.
+__device__ __forceinline__ void put_pair(uint8_t* rows, int row, int q, uint4 a, uint4 b, bool wide) {
+  if (wide) {
+    if (row & 1) {
+      const uint4 t = a;
+      a = b;
+      b = t;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(rows + (swz(row, 2 * q) & ~16u)), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(rows + swz(row, 2 * q)) = a;
+    *reinterpret_cast<uint4*>(rows + swz(row, 2 * q + 1)) = b;
+  }
+}
+
+
 // ---- operand tiles and scales: one CTA per (tile, KV head) for the keys and one
 // for the values; also the row blocks' tile ranges, spread over the latter's warps.
 template <int D>
@@ -225,13 +245,14 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
   }
   // K page [D/16][16 tokens][16 B] and V page [D][16 B]: D chunks each per block.
   // D = 256: a thread per chunk; below, 256 / D blocks at once.
-  constexpr int kAt = 256 / D;
+  constexpr int kAt = 256 / D, kIn = kBlk / kAt;
+  const bool wide = (reinterpret_cast<uintptr_t>(ws) & 31) == 0;
   const int sub = tid / D, c = tid % D;
 #pragma unroll
-  for (int i0 = 0; i0 < kBlk; i0 += 4 * kAt) {
-    uint4 x[4];
+  for (int i0 = 0; i0 < kBlk; i0 += kIn * kAt) {
+    uint4 x[kIn];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kIn; ++u) {
       int ph = -1;
 #pragma unroll
       for (int s = 0; s < kAt; ++s)
@@ -241,25 +262,20 @@ __global__ void __launch_bounds__(256) block_tiles_kernel(const __grid_constant_
         x[u] = __ldg(reinterpret_cast<const uint4*>((keys ? p.k_cache : p.v_cache) + ((size_t)ph * p.Hkv + kvh) * (D * kBS)) + c);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kIn; ++u) {
       const int i = i0 + u * kAt + sub;
-      if (i >= kBlk) continue;
+      uint4 h0, h1;
       if (keys) {
         const int dc = c / kBS, key = i * kBS + c % kBS;
-        uint8_t* atom = kt + (size_t)(dc / 4) * (kKeys * 128);
-        *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4))) =
-            make_uint4(bf16x2_codes(x[u].x, 0), bf16x2_codes(x[u].x, 2), bf16x2_codes(x[u].y, 0), bf16x2_codes(x[u].y, 2));
-        *reinterpret_cast<uint4*>(atom + swz(key, 2 * (dc % 4) + 1)) =
-            make_uint4(bf16x2_codes(x[u].z, 0), bf16x2_codes(x[u].z, 2), bf16x2_codes(x[u].w, 0), bf16x2_codes(x[u].w, 2));
+        h0 = make_uint4(bf16x2_codes(x[u].x, 0), bf16x2_codes(x[u].x, 2), bf16x2_codes(x[u].y, 0), bf16x2_codes(x[u].y, 2));
+        h1 = make_uint4(bf16x2_codes(x[u].z, 0), bf16x2_codes(x[u].z, 2), bf16x2_codes(x[u].w, 0), bf16x2_codes(x[u].w, 2));
+        put_pair(kt + (size_t)(dc / 4) * (kKeys * 128), key, dc % 4, h0, h1, wide);
       } else {
-        uint8_t* half = vt + (size_t)(i / 4) * (D * 128);
-        uint4 h0, h1;
         s8x4_to_f16(x[u].x, h0.x, h0.y);
         s8x4_to_f16(x[u].y, h0.z, h0.w);
         s8x4_to_f16(x[u].z, h1.x, h1.y);
         s8x4_to_f16(x[u].w, h1.z, h1.w);
-        *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4))) = h0;
-        *reinterpret_cast<uint4*>(half + swz(c, 2 * (i % 4) + 1)) = h1;
+        put_pair(vt + (size_t)(i / 4) * (D * 128), c, i % 4, h0, h1, wide);
       }
     }
   }

@@ -464,6 +464,24 @@ def test_chunk_few_rows(D, rows):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+def test_chunk_workspace_at_sixteen_bytes(D):
+    """A workspace on a 16-byte boundary that is no 32-byte boundary gives the same bits."""
+    rng = np.random.default_rng(D)
+    H, C, Hq, Hkv = 300, 260, 4, 2
+    table, nb = tables(rng, [H + C])
+    c, q = Cache(nb, Hkv, D).random(rng), dev_bf16(rng.standard_normal((C, Hq, D)))
+    n = i8.block_prefix_workspace(H, C, Hq, Hkv, D).numel()
+    room = torch.empty(n + 64, dtype=torch.uint8, device="cuda")
+    outs = []
+    for shift in (0, 16):
+        at = -room.data_ptr() % 32 + shift
+        out = torch.full((C, Hq, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+        i8.block_prefix_attn(out, q, **upload(c), block_table=dev(table[0]), history_len=H, workspace=room[at:at + n])
+        outs.append(out)
+    assert torch.equal(*outs) and i8.device_error() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("kw", VARIANTS)
 def test_chunk_row_groups_of_sixteen(D, kw):
     """A CTA per (group, KV head), and the evenly cut list of long histories."""
