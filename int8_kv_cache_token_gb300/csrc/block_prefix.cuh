@@ -4,7 +4,7 @@
 // Row (token j, query head h) at position pos = H + j over its visible keys:
 //   x_t = scale q . (sK cK_t),  s_t = cap tanh(x_t / cap) (or x_t) - slope_h |pos - t|
 //   O = sum_t softmax(s)_t sV cV_t
-// as in block_decode.cu: u_t = s_t log2 e + log2 sV, weights w_t = 2^(u_t - M),
+// as in block_decode.cuh: u_t = s_t log2 e + log2 sV, weights w_t = 2^(u_t - M),
 // O = sum w cV / sum w / sV, so the two scales of a 16-key block are one multiply
 // and one addend of its 16 scores, and the products below run on the bare codes.
 //
@@ -36,17 +36,17 @@
 // order, which is what lets W share its S slot with the S after next.
 //
 // What bounds it, measured on a GB300 (2048 rows over 16384 keys).  24/4 heads of
-// 256: 550 us, 1590 TFLOP/s, 0.81 of the dense peak; a tile's products want 2048
+// 256: 499 us, 1760 TFLOP/s, 0.90 of the dense peak; a tile's products want 2048
 // cycles and take about 2600, because Q K^T with both operands in shared memory
 // reads 128 bytes a cycle, all that shared memory gives, beside the tile copies.
-// With a cap 641 us: the polynomial makes the softmax of a tile (3700 cycles) the
+// With a cap 600 us: the polynomial makes the softmax of a tile (3700 cycles) the
 // longest part of the S -> W -> O chain, of which two are in flight.  32/8 heads of
-// 128: 442 us, 1320 TFLOP/s: the chain again, 1024 cycles of exponentials (16 a
+// 128: 409 us, 1430 TFLOP/s: the chain again, 1024 cycles of exponentials (16 a
 // cycle) for 1024 cycles of products.  Tried and dropped: exponentials of one pair
-// in four by a polynomial (FMA issue was the next limit: 520 against 462 us at
+// in four by a polynomial (FMA issue was the next limit: 520 against then 462 us at
 // head_dim 128), and the maximum, the scores and the weights in one pass that is
 // repeated when the maximum moves (its branches keep the compiler from overlapping
-// the 32-column steps: 594 against 550 us at 256, 592 against 442 us at 128).
+// the 32-column steps: 594 against then 550 us at 256, 592 against 442 us at 128).
 #pragma once
 
 #include <type_traits>

@@ -453,6 +453,25 @@ def test_chunk_rows_at_the_limits_of_both_routes():
             _chunk(128, 8, 4, H, 40, seed=H, window=window)
 
 
+def test_sixteen_rows_bad_tables_are_recorded():
+    """Passes of sixteen rows: a table entry outside the pool of a visible block, in a decode and in a chunk."""
+    rng = np.random.default_rng(16)
+    H, C, Hq, Hkv, D = 11000, 25, 32, 2, 64
+    table, nb = tables(rng, [H + C])
+    c = Cache(nb, Hkv, D).random(rng)
+    q = dev_bf16(rng.standard_normal((C, Hq, D)))
+    out = torch.empty((C, Hq, D), dtype=torch.bfloat16, device="cuda")
+    wide = np.concatenate([table, np.zeros((1, 4000), np.int32)], 1)  # enough blocks for sixteen rows per pass
+    for bad in (None, nb, -1):
+        t, w = table.copy(), wide.copy()
+        if bad is not None:
+            t[0, 300] = w[0, 300] = bad
+        i8.block_decode_attn(out[:1], q[:1], **upload(c), block_tables=dev(w), seq_lens=dev(np.int32([H])))
+        assert i8.device_error() == (0 if bad is None else 2)
+        i8.block_prefix_attn(out[:5], q[:5], **upload(c), block_table=dev(t[0]), history_len=H)
+        assert i8.device_error() == (0 if bad is None else 2)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("rows", [1, 7, 8, 9, 15, 16, 17, 31, 33, 64])
 def test_chunk_few_rows(D, rows):
