@@ -453,6 +453,32 @@ def test_chunk_rows_at_the_limits_of_both_routes():
             _chunk(128, 8, 4, H, 40, seed=H, window=window)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sixteen_rows_strided_and_replayed(D):
+    """Passes of sixteen rows on a strided q, captured and replayed with other values: the bits of an eager call."""
+    rng = np.random.default_rng(D)
+    lens, Hq, Hkv = [700, 90, 0, 333], 24, 2
+    table, nb = tables(rng, lens)
+    wide = np.concatenate([table, np.full((len(lens), 1000), nb, np.int32)], 1)
+    c, table = upload(Cache(nb, Hkv, D).random(rng)), dev(wide)
+    fused = torch.zeros((len(lens), (Hq + 2 * Hkv) * D), dtype=torch.bfloat16, device="cuda")
+    q, sl = fused[:, :Hq * D].view(len(lens), Hq, D), dev(np.int32([16, 16, 0, 16]))  # the third has no page
+    ws = i8.block_decode_workspace(len(lens), Hq, Hkv, D, wide.shape[1])
+    out, again = (torch.empty((len(lens), Hq, D), dtype=torch.float32, device="cuda") for _ in range(2))
+    i8.block_decode_attn(out, q, **c, block_tables=table, seq_lens=sl, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        i8.block_decode_attn(out, q, **c, block_tables=table, seq_lens=sl, workspace=ws)
+    for n in (lens, [33, 1, 0, 330], lens):
+        q.copy_(dev_bf16(rng.standard_normal((len(lens), Hq, D))))
+        sl.copy_(dev(np.int32(n)))
+        g.replay()
+        i8.block_decode_attn(again, q.contiguous(), **c, block_tables=table, seq_lens=sl)
+        assert torch.equal(out, again) and out.abs().sum() > 0
+    assert i8.device_error() == 0
+
+
 def test_sixteen_rows_bad_tables_are_recorded():
     """Passes of sixteen rows: a table entry outside the pool of a visible block, in a decode and in a chunk."""
     rng = np.random.default_rng(16)
